@@ -7,6 +7,8 @@ first call does, and raises if the library is missing or no GPU is present.
 """
 from ._binding import (  # noqa: F401
     AttnError,
+    attn_append_paged,
+    attn_append_paged_fp8,
     attn_bwd,
     attn_bwd_block_sparse,
     attn_bwd_varlen,
@@ -29,7 +31,10 @@ from ._binding import (  # noqa: F401
     attn_fwd_varlen_workspace_size,
     attn_fwd_window,
     attn_get_device_error,
+    attn_rope,
+    attn_rope_bwd,
     attn_strerror,
     library_path,
     load_library,
 )
+from .rope import rope_frequencies  # noqa: F401

@@ -33,6 +33,8 @@ _P = ctypes.c_void_p
 _I = ctypes.c_int
 _F = ctypes.c_float
 _SZ = ctypes.c_size_t
+_LL = ctypes.c_longlong
+_LL6, _LL12 = _LL * 6, _LL * 12
 SIGNATURES = {
     "attn_fwd": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F, _P]),
     "attn_fwd_masked": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F, _P, _P]),
@@ -67,6 +69,10 @@ SIGNATURES = {
     "attn_bwd_varlen": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I,
                              ctypes.c_longlong, ctypes.c_longlong, _I, _I, _I, _I, _F, _P, _SZ,
                              _P]),
+    "attn_rope": (_I, [_P] * 6 + [_LL] + [_I] * 7 + [_F, _P, _P]),
+    "attn_rope_bwd": (_I, [_P] * 6 + [_LL] + [_I] * 7 + [_F, _P, _P]),
+    "attn_append_paged": (_I, [_P] * 11 + [_I] * 4 + [_LL] + [_I] * 5 + [_F, _P, _P]),
+    "attn_append_paged_fp8": (_I, [_P] * 13 + [_I] * 4 + [_LL] + [_I] * 5 + [_F, _P, _P]),
     "attn_get_device_error": (_I, [_P, ctypes.POINTER(ctypes.c_uint)]),
     "attn_strerror": (ctypes.c_char_p, [_I]),
     "attn_split_tokens": (_I, []),
@@ -720,6 +726,230 @@ def attn_decode_paged_noalloc(q, k_cache, v_cache, block_table, seq_lens, scale,
         _stream(stream))
     _check(st, "attn_decode_paged_noalloc")
     return out, lse
+
+
+# The calls below check and marshal their arguments with as few tensor attribute reads as
+# they can: a decode step's kernels take a few microseconds each, and so may the host.
+
+def _device_index(first, *rest):
+    """The index of the CUDA device that every tensor given (None: left out) lives on."""
+    index = first.get_device()
+    if index < 0:
+        raise ValueError("tensors must be CUDA tensors (device memory)")
+    for t in rest:
+        if t is not None and t.get_device() != index:
+            raise ValueError("tensors must be CUDA tensors (device memory) of one device")
+    return index
+
+
+def _int32(t, shape, name):
+    """Raise unless t is a contiguous int32 tensor of this shape."""
+    import torch
+    if t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous int32 {list(shape)}")
+
+
+def _raw_stream(stream, index):
+    """The handle of the stream a call runs on: the given one, or the device's current one."""
+    import torch
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(index)
+    if stream.device.index != index:
+        raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{index}")
+    return stream.cuda_stream
+
+
+def _new(like, shape, dtype, stream):
+    """A new buffer on ``like``'s device for work on ``stream`` (None: the current one),
+    allocated there, so that the allocator hands its memory on only behind that work."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _launch(name, index, *args):
+    """Call the library's function ``name`` with the device current."""
+    import torch
+    fn = getattr(_lib or load_library(), name)
+    if torch._C._cuda_getDevice() == index:
+        st = fn(*args)
+    else:
+        with torch.cuda.device(index):
+            st = fn(*args)
+    if st != ATTN_OK:
+        raise AttnError(st, name)
+
+
+def _rope_freq(inv_freq, d):
+    """rotary_dim of a frequency table."""
+    import torch
+    if inv_freq.dtype is not torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+        raise ValueError("inv_freq must be contiguous float64 [rotary_dim / 2]")
+    rot = 2 * inv_freq.shape[0]
+    if rot > d:
+        raise ValueError(f"inv_freq turns {rot} elements of a head of {d}")
+    return rot
+
+
+def _rope(name, q, k, inv_freq, positions, interleaved, mscale, q_out, k_out, stream):
+    import torch
+    bf16 = torch.bfloat16
+    index = _device_index(q, k, inv_freq, positions, q_out, k_out)
+    raw = _raw_stream(stream, index)
+    shape = q.shape
+    if len(shape) != 4:
+        raise ValueError("q must be [B, Hq, S, d]")
+    B, Hq, S, d = shape
+    sq = q.stride()
+    if q.dtype is not bf16 or sq[3] != 1:
+        raise ValueError("q must be bfloat16 with contiguous rows")
+    if q_out is None:
+        q_out = _new(q, shape, bf16, stream)
+    elif q_out.shape != shape or q_out.dtype is not bf16 or q_out.stride(3) != 1:
+        raise ValueError("q_out must be bfloat16 of q's shape with contiguous rows")
+    so = q_out.stride()
+    if k is not None:
+        kshape, sk = k.shape, k.stride()
+        if len(kshape) != 4:
+            raise ValueError("k must be [B, Hkv, S, d]")
+        Hkv = kshape[1]
+        if kshape != (B, Hkv, S, d) or k.dtype is not bf16 or sk[3] != 1:
+            raise ValueError("k must be bfloat16 [B, Hkv, S, d] with contiguous rows")
+        if k_out is None:
+            k_out = _new(k, kshape, bf16, stream)
+        elif k_out.shape != kshape or k_out.dtype is not bf16 or k_out.stride(3) != 1:
+            raise ValueError("k_out must be bfloat16 of k's shape with contiguous rows")
+        sko = k_out.stride()
+        strides = sq[:3] + sk[:3] + so[:3] + sko[:3]
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    else:
+        Hkv = 0
+        strides = sq[:3] + (0, 0, 0) + so[:3] + (0, 0, 0)
+    rot = _rope_freq(inv_freq, d)
+    pos_stride = 0
+    if positions is not None:
+        pshape = positions.shape
+        if positions.dtype is not torch.int32 or (pshape != (S,) and pshape != (B, S)) \
+                or (S > 1 and positions.stride(-1) != 1):
+            raise ValueError("positions must be int32 [S] or [B, S] with contiguous rows")
+        if len(pshape) == 2 and B > 1:
+            pos_stride = positions.stride(0)
+    _launch(name, index, q.data_ptr(), _addr(k), q_out.data_ptr(), _addr(k_out),
+            inv_freq.data_ptr(), _addr(positions), pos_stride, B, Hq, Hkv, S, d, rot,
+            1 if interleaved else 0, mscale, _LL12(*strides), raw)
+    return q_out, k_out
+
+
+def attn_rope(q, k, inv_freq, positions=None, interleaved: bool = False, mscale: float = 1.0,
+              q_out=None, k_out=None, stream=None):
+    """Rotary positions: q [B,Hq,S,d], k [B,Hkv,S,d] or None, bf16 CUDA tensors of any
+    (batch, head, row) strides; inv_freq float64 [rotary_dim/2] on the device (see
+    rope_frequencies); positions int32 [S] or [B,S], None: 0..S-1.  Returns (q_out, k_out),
+    contiguous unless given; q_out=q, k_out=k turn in place.  A packed [tokens, H, d] tensor x
+    is passed as x.transpose(0, 1)[None]."""
+    return _rope("attn_rope", q, k, inv_freq, positions, interleaved, mscale, q_out, k_out, stream)
+
+
+def attn_rope_bwd(dq, dk, inv_freq, positions=None, interleaved: bool = False,
+                  mscale: float = 1.0, q_out=None, k_out=None, stream=None):
+    """The gradient of attn_rope: gradients of its outputs in, gradients of its inputs out
+    (other arguments as the forward's)."""
+    return _rope("attn_rope_bwd", dq, dk, inv_freq, positions, interleaved, mscale, q_out, k_out,
+                 stream)
+
+
+def _append(name, k, v, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_seqlens, q,
+            inv_freq, positions, interleaved, mscale, q_out, stream):
+    import torch
+    bf16 = torch.bfloat16
+    fp8 = k_scale is not None
+    index = _device_index(k, v, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
+                          cu_seqlens, q, inv_freq, positions, q_out)
+    raw = _raw_stream(stream, index)
+    shape, cache, table = k.shape, k_cache.shape, block_table.shape
+    if len(shape) != 3 or v.shape != shape:
+        raise ValueError("k and v must be [total, Hkv, d]")
+    total, Hkv, d = shape
+    if len(cache) != 4 or v_cache.shape != cache or cache[2] != Hkv or cache[3] != d \
+            or not k_cache.is_contiguous() or not v_cache.is_contiguous():
+        raise ValueError("caches must be contiguous [num_pages, page_size, Hkv, d]")
+    dtype = torch.uint8 if fp8 else bf16
+    if k_cache.dtype is not dtype or v_cache.dtype is not dtype:
+        raise ValueError(f"the caches must be {dtype}")
+    scales = ()
+    if fp8:
+        for t in (k_scale, v_scale):
+            if t.dtype is not torch.float32 or t.shape != (cache[0], Hkv) \
+                    or not t.is_contiguous():
+                raise ValueError("scales must be contiguous float32 [num_pages, Hkv]")
+        scales = (k_scale.data_ptr(), v_scale.data_ptr())
+    if len(table) != 2 or block_table.dtype is not torch.int32 or not block_table.is_contiguous():
+        raise ValueError("block_table must be contiguous int32 [B, max_pages_per_seq]")
+    B = table[0]
+    _int32(seq_lens, (B,), "seq_lens")
+    if cu_seqlens is not None:
+        _int32(cu_seqlens, (B + 1,), "cu_seqlens")
+    elif total != B:
+        raise ValueError("without cu_seqlens k and v hold one token per sequence")
+    if positions is not None:
+        _int32(positions, (total,), "positions")
+    rot = 0 if inv_freq is None else _rope_freq(inv_freq, d)
+    sk, sv = k.stride(), v.stride()
+    if k.dtype is not bf16 or v.dtype is not bf16 or sk[2] != 1 or sv[2] != 1:
+        raise ValueError("k and v must be bfloat16 with contiguous rows")
+    sq, Hq = (0, 0), 0
+    if q is not None:
+        qshape, sq = q.shape, q.stride()
+        if len(qshape) != 3 or qshape[0] != total or qshape[2] != d or q.dtype is not bf16 \
+                or sq[2] != 1:
+            raise ValueError("q must be bfloat16 [total, Hq, d] with contiguous rows")
+        Hq = qshape[1]
+        if q_out is None:
+            q_out = _new(q, qshape, bf16, stream)
+        elif q_out.shape != qshape or q_out.dtype is not bf16 or not q_out.is_contiguous():
+            raise ValueError("q_out must be contiguous bfloat16 of q's shape")
+        elif q_out.data_ptr() == q.data_ptr() and not q.is_contiguous():
+            raise ValueError("q_out may be q itself only when q is contiguous")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    _launch(name, index, _addr(q), k.data_ptr(), v.data_ptr(), _addr(q_out), k_cache.data_ptr(),
+            v_cache.data_ptr(), *scales, block_table.data_ptr(), _addr(cu_seqlens),
+            seq_lens.data_ptr(), _addr(positions), _addr(inv_freq), cache[1], B, Hq, Hkv, total,
+            table[1], cache[0], d, rot, 1 if interleaved else 0, mscale,
+            _LL6(*sq[:2], *sk[:2], *sv[:2]), raw)
+    return q_out
+
+
+def attn_append_paged(k, v, k_cache, v_cache, block_table, seq_lens, cu_seqlens=None, q=None,
+                      inv_freq=None, positions=None, interleaved: bool = False,
+                      mscale: float = 1.0, q_out=None, stream=None):
+    """Write new tokens k, v [total, Hkv, d] bf16 (views of a fused projection are fine) into
+    the paged cache [num_pages, page_size, Hkv, d], as the last ones of their sequences:
+    seq_lens [B] counts them in, cu_seqlens [B+1] gives each sequence's tokens (None: one token
+    per sequence).  K and, where given, q [total, Hq, d] are rotated on the way (inv_freq as
+    attn_rope; None: not at all).  Returns the rotated queries, contiguous, or None."""
+    return _append("attn_append_paged", k, v, k_cache, v_cache, None, None, block_table, seq_lens,
+                   cu_seqlens, q, inv_freq, positions, interleaved, mscale, q_out, stream)
+
+
+def attn_append_paged_fp8(k, v, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
+                          cu_seqlens=None, q=None, inv_freq=None, positions=None,
+                          interleaved: bool = False, mscale: float = 1.0, q_out=None,
+                          stream=None):
+    """attn_append_paged into an E4M3 cache (uint8 codes) with the given float32 scales
+    [num_pages, Hkv], which are read and stay as they are."""
+    if k_scale is None or v_scale is None:
+        raise ValueError("an E4M3 cache needs k_scale and v_scale")
+    return _append("attn_append_paged_fp8", k, v, k_cache, v_cache, k_scale, v_scale, block_table,
+                   seq_lens, cu_seqlens, q, inv_freq, positions, interleaved, mscale,
+                   q_out, stream)
 
 
 def attn_get_device_error(stream=None):

@@ -8,6 +8,7 @@
 #include <cstdint>
 #include <cstring>
 #include <mutex>
+#include <utility>
 #include <vector>
 
 #include "attn.h"
@@ -1294,3 +1295,5 @@ extern "C" int attn_decode_paged_noalloc(const void* q, const void* k_cache, con
                            max_pages_per_seq, num_pages, scale, o, lse, scratch,
                            (size_t)ATTN_NOALLOC_SCRATCH_BYTES, stream);
 }
+
+#include "rope_api.cuh"

@@ -555,6 +555,112 @@ int attn_bwd_varlen(const void* q, const void* k, const void* v, const void* o, 
                     long long total_k, int max_seqlen_q, int max_seqlen_k, int d, int causal,
                     float scale, void* workspace, size_t workspace_bytes, attn_stream_t stream);
 
+/*
+ * attn_rope -- rotary positions of Q and K, out of place or in place.
+ *   A head row of d elements has rotary_dim turned elements, read as pairs
+ *   (a, b): elements (i, i + rotary_dim / 2) in the half layout (interleaved =
+ *   0), (2i, 2i + 1) in the interleaved one (1); the other elements are copied.
+ *   With t = position * inv_freq[i] (formed and reduced in float64),
+ *     a' = mscale (a cos t - b sin t),  b' = mscale (a sin t + b cos t),
+ *   rounded once to bf16.
+ *   q, q_out [B, Hq, S, d], k, k_out [B, Hkv, S, d] bf16.  Hkv may be 0 (k and
+ *   k_out NULL): queries only.
+ *   inv_freq  [rotary_dim / 2] float64 device array: radians per position of
+ *             each pair, whatever scheme made them (bases, stretched or ramped
+ *             frequencies for long contexts); 8-byte aligned.
+ *   positions int32 device array, any values: row s of sequence b is at
+ *             positions[b * pos_stride + s] (pos_stride 0: shared by the
+ *             batch); NULL: s.
+ *   strides   HOST array of 12 element strides, the (batch, head, row) strides
+ *             of q, k, q_out and k_out, or NULL when all are contiguous.  Rows
+ *             themselves are contiguous; strides are multiples of 8 (16-byte
+ *             pieces), not negative, and the outputs' rows may not overlap.
+ *             Q and K may thus be views of a fused [B, S, heads, d] projection.
+ *   q_out may be q with the same strides (in place), likewise k_out and k;
+ *   any other overlap of an input with an output gives undefined values.
+ *   rotary_dim a multiple of 16 in [16, d]; d in {64, 128}; S >= 0; B * S <
+ *   2^31; mscale finite.
+ * Errors: INVALID_ARG, UNSUPPORTED (d, rotary_dim), ALIGNMENT, CUDA.
+ */
+int attn_rope(const void* q, const void* k, void* q_out, void* k_out, const double* inv_freq,
+              const int32_t* positions, long long pos_stride, int B, int Hq, int Hkv, int S, int d,
+              int rotary_dim, int interleaved, float mscale, const long long* strides,
+              attn_stream_t stream);
+
+/*
+ * attn_rope_bwd -- the gradient of attn_rope: the same map turned by -t.
+ *   dq, dk: gradients of attn_rope's outputs; dq_out, dk_out: gradients of its
+ *   inputs.  Everything else, in place included, as attn_rope.
+ */
+int attn_rope_bwd(const void* dq, const void* dk, void* dq_out, void* dk_out,
+                  const double* inv_freq, const int32_t* positions, long long pos_stride, int B,
+                  int Hq, int Hkv, int S, int d, int rotary_dim, int interleaved, float mscale,
+                  const long long* strides, attn_stream_t stream);
+
+/*
+ * attn_append_paged -- write new keys and values into a paged cache, rotating
+ * K (and the queries that come with them) on the way.
+ * Source of the cache layout: "Attention Kernel", section "Paged 与 ragged KV".
+ *   k, v     [total, Hkv, d] bf16: the packed new tokens
+ *   q        [total, Hq, d] bf16 or NULL (Hq = 0); q_out [total, Hq, d] bf16,
+ *            contiguous, receives the rotated queries (may be q itself when q
+ *            is contiguous)
+ *   strides  HOST array of 6 element strides, (token, head) of q, k and v,
+ *            multiples of 8 and not negative, or NULL when contiguous: the
+ *            three may be views of one fused projection
+ *   k_cache, v_cache [num_pages, page_size, Hkv, d] bf16
+ *   block_table [B, max_pages_per_seq] int32 (entries that no new token falls
+ *            on are not read)
+ *   cu_seqlens [B + 1] int32: sequence b owns tokens [cu[b], cu[b+1]); NULL:
+ *            one token per sequence, total = B
+ *   seq_lens [B] int32: keys of each sequence WITH the new ones, as
+ *            attn_fwd_paged's seq_lens_k and attn_decode_paged's seq_lens
+ *            count them: the new tokens are the last ones.  Without cu_seqlens
+ *            a sequence of length 0 is an idle row of the batch: nothing of it
+ *            is written.
+ *   positions [total] int32 or NULL: the angle's position of each token where
+ *            it is not the token's place in its sequence
+ *   inv_freq, rotary_dim, interleaved, mscale: as attn_rope; inv_freq NULL:
+ *            nothing turns (mscale is not applied either)
+ *   page_size a positive multiple of 16 (<= 256); d in {64, 128}.
+ *   Two tokens with the same place (a page listed twice) are written in no
+ *   fixed order.  Tokens behind the last sequence are left alone, as are
+ *   their q_out rows, and every other slot of the cache.
+ * Device-side faults: a page id outside [0, num_pages) is skipped (its keys
+ * and values are not written) and flags ATTN_DEVERR_BAD_PAGE; a sequence whose
+ * length is below its number of new tokens or over max_pages_per_seq *
+ * page_size, or whose offsets leave [0, total], is skipped, q_out included,
+ * and flags ATTN_DEVERR_BAD_LENGTH, and so do offsets that decrease (tokens
+ * next to them may be skipped).
+ * Errors: INVALID_ARG, UNSUPPORTED (d, rotary_dim, page_size), ALIGNMENT, CUDA.
+ */
+int attn_append_paged(const void* q, const void* k, const void* v, void* q_out, void* k_cache,
+                      void* v_cache, const int32_t* block_table, const int32_t* cu_seqlens,
+                      const int32_t* seq_lens, const int32_t* positions, const double* inv_freq,
+                      int page_size, int B, int Hq, int Hkv, long long total,
+                      int max_pages_per_seq, int num_pages, int d, int rotary_dim,
+                      int interleaved, float mscale, const long long* strides,
+                      attn_stream_t stream);
+
+/*
+ * attn_append_paged_fp8 -- attn_append_paged into an E4M3 cache with one scale
+ * per (page, KV head), the layout that attn_decode_paged_fp8 reads.
+ *   k_scale, v_scale [num_pages, Hkv] float32: read, not changed.  The code
+ *   written is the E4M3 value nearest to x / scale (x the rotated key, or the
+ *   value, in float32; ties to even), values beyond +-448 becoming +-448; a
+ *   scale of 0 writes zeros.  Inputs and scales must be finite.
+ * Everything else as attn_append_paged; INVALID_ARG also for a NULL scale
+ * array, ALIGNMENT for scales not 4-byte aligned.
+ */
+int attn_append_paged_fp8(const void* q, const void* k, const void* v, void* q_out, void* k_cache,
+                          void* v_cache, const float* k_scale, const float* v_scale,
+                          const int32_t* block_table, const int32_t* cu_seqlens,
+                          const int32_t* seq_lens, const int32_t* positions,
+                          const double* inv_freq, int page_size, int B, int Hq, int Hkv,
+                          long long total, int max_pages_per_seq, int num_pages, int d,
+                          int rotary_dim, int interleaved, float mscale, const long long* strides,
+                          attn_stream_t stream);
+
 /* attn_strerror -- static description of an attn_status value. */
 const char* attn_strerror(int status);
 
