@@ -14,6 +14,8 @@ from ._binding import (  # noqa: F401
     attn_bwd_varlen,
     attn_bwd_varlen_workspace_size,
     attn_bwd_window,
+    attn_bwd_window_sinks,
+    attn_bwd_window_sinks_workspace_size,
     attn_bwd_workspace_size,
     attn_fwd_block_sparse,
     attn_decode_paged,
@@ -27,9 +29,11 @@ from ._binding import (  # noqa: F401
     attn_fwd_paged,
     attn_fwd_paged_fp8,
     attn_fwd_paged_fp8_workspace_size,
+    attn_fwd_paged_window,
     attn_fwd_varlen,
     attn_fwd_varlen_workspace_size,
     attn_fwd_window,
+    attn_fwd_window_sinks,
     attn_get_device_error,
     attn_rope,
     attn_rope_bwd,

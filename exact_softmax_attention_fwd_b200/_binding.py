@@ -69,6 +69,11 @@ SIGNATURES = {
     "attn_bwd_varlen": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I,
                              ctypes.c_longlong, ctypes.c_longlong, _I, _I, _I, _I, _F, _P, _SZ,
                              _P]),
+    "attn_fwd_window_sinks": (_I, [_P] * 5 + [_I] * 6 + [_F, _P, _I, _I, _P]),
+    "attn_fwd_paged_window": (_I, [_P] * 6 + [_I] * 4 + [_LL] + [_I] * 4 + [_F, _I, _I, _P, _P, _P,
+                                                                           _SZ, _P]),
+    "attn_bwd_window_sinks_workspace_size": (_SZ, [_I] * 8),
+    "attn_bwd_window_sinks": (_I, [_P] * 9 + [_I] * 6 + [_F, _P, _I, _I, _P, _SZ, _P]),
     "attn_rope": (_I, [_P] * 6 + [_LL] + [_I] * 7 + [_F, _P, _P]),
     "attn_rope_bwd": (_I, [_P] * 6 + [_LL] + [_I] * 7 + [_F, _P, _P]),
     "attn_append_paged": (_I, [_P] * 11 + [_I] * 4 + [_LL] + [_I] * 5 + [_F, _P, _P]),
@@ -843,7 +848,7 @@ def _rope(name, q, k, inv_freq, positions, interleaved, mscale, q_out, k_out, st
             pos_stride = positions.stride(0)
     _launch(name, index, q.data_ptr(), _addr(k), q_out.data_ptr(), _addr(k_out),
             inv_freq.data_ptr(), _addr(positions), pos_stride, B, Hq, Hkv, S, d, rot,
-            1 if interleaved else 0, mscale, _LL12(*strides), raw)
+            1 if interleaved else 0, float(mscale), _LL12(*strides), raw)
     return q_out, k_out
 
 
@@ -922,7 +927,7 @@ def _append(name, k, v, k_cache, v_cache, k_scale, v_scale, block_table, seq_len
     _launch(name, index, _addr(q), k.data_ptr(), v.data_ptr(), _addr(q_out), k_cache.data_ptr(),
             v_cache.data_ptr(), *scales, block_table.data_ptr(), _addr(cu_seqlens),
             seq_lens.data_ptr(), _addr(positions), _addr(inv_freq), cache[1], B, Hq, Hkv, total,
-            table[1], cache[0], d, rot, 1 if interleaved else 0, mscale,
+            table[1], cache[0], d, rot, 1 if interleaved else 0, float(mscale),
             _LL6(*sq[:2], *sk[:2], *sv[:2]), raw)
     return q_out
 
@@ -950,6 +955,123 @@ def attn_append_paged_fp8(k, v, k_cache, v_cache, k_scale, v_scale, block_table,
     return _append("attn_append_paged_fp8", k, v, k_cache, v_cache, k_scale, v_scale, block_table,
                    seq_lens, cu_seqlens, q, inv_freq, positions, interleaved, mscale,
                    q_out, stream)
+
+
+def _buffer(t, like, shape, dtype, stream, name):
+    """A caller's output buffer, checked, or a new one."""
+    if t is None:
+        return _new(like, shape, dtype, stream)
+    if t.shape != shape or t.dtype is not dtype or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
+    return t
+
+
+def _workspace(t, like, need, stream):
+    """(address, bytes) of a caller's workspace, or of a new one (kept alive by the third)."""
+    import torch
+    if t is None:
+        t = _new(like, (max(need, 16),), torch.uint8, stream)
+    return t.data_ptr(), t.numel() * t.element_size(), t
+
+
+def _dense_shapes(q, k, v, k_lens):
+    """(B, Hq, Hkv, Sq, Sk, d) of contiguous bf16 q [B,Hq,Sq,d] and k, v [B,Hkv,Sk,d]."""
+    import torch
+    bf16 = torch.bfloat16
+    qs, ks = q.shape, k.shape
+    if len(qs) != 4 or len(ks) != 4 or v.shape != ks or ks[0] != qs[0] or ks[3] != qs[3]:
+        raise ValueError("q must be [B, Hq, Sq, d], k and v [B, Hkv, Sk, d]")
+    for t in (q, k, v):
+        if t.dtype is not bf16 or not t.is_contiguous():
+            raise ValueError("q, k, v must be contiguous bfloat16")
+    if k_lens is not None:
+        _int32(k_lens, (qs[0],), "k_lens")
+    return qs[0], qs[1], ks[1], qs[2], ks[2], qs[3]
+
+
+def attn_fwd_window_sinks(q, k, v, scale: float, window: int, sinks: int = 0, k_lens=None,
+                          out=None, lse=None, return_lse: bool = True, stream=None):
+    """Causal prefill with a sliding window (0: none) and the first ``sinks`` tokens visible
+    throughout; q [B,Hq,Sq,d], k/v [B,Hkv,Sk,d] bf16 CUDA tensors (layouts as
+    attn_fwd_masked)."""
+    import torch
+    index = _device_index(q, k, v, k_lens, out, lse)
+    raw = _raw_stream(stream, index)
+    B, Hq, Hkv, Sq, Sk, d = _dense_shapes(q, k, v, k_lens)
+    out = _buffer(out, q, q.shape, torch.bfloat16, stream, "out")
+    if lse is not None or return_lse:
+        lse = _buffer(lse, q, (B, Hq, Sq), torch.float32, stream, "lse")
+    _launch("attn_fwd_window_sinks", index, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+            out.data_ptr(), _addr(lse), B, Hq, Hkv, Sq, Sk, d, float(scale), _addr(k_lens),
+            int(window), int(sinks),
+            raw)
+    return out, lse
+
+
+def attn_bwd_window_sinks_workspace_size(B: int, Hq: int, Hkv: int, Sq: int, Sk: int, d: int,
+                                         window: int, sinks: int) -> int:
+    return int(load_library().attn_bwd_window_sinks_workspace_size(B, Hq, Hkv, Sq, Sk, d, window,
+                                                                   sinks))
+
+
+def attn_bwd_window_sinks(q, k, v, o, lse, d_o, scale: float, window: int, sinks: int = 0,
+                          k_lens=None, dq=None, dk=None, dv=None, workspace=None, stream=None):
+    """dQ, dK, dV of attn_fwd_window_sinks.  o, lse as the forward returned them for the same
+    scale, window, sinks and k_lens; d_o like o."""
+    import torch
+    bf16 = torch.bfloat16
+    index = _device_index(q, k, v, o, lse, d_o, k_lens, dq, dk, dv, workspace)
+    raw = _raw_stream(stream, index)
+    B, Hq, Hkv, Sq, Sk, d = _dense_shapes(q, k, v, k_lens)
+    for t in (o, d_o):
+        if t.shape != q.shape or t.dtype is not bf16 or not t.is_contiguous():
+            raise ValueError("o and d_o must be contiguous bfloat16 of q's shape")
+    if lse.dtype is not torch.float32 or lse.shape != (B, Hq, Sq) or not lse.is_contiguous():
+        raise ValueError("lse must be contiguous float32 [B, Hq, Sq]")
+    dq = _buffer(dq, q, q.shape, bf16, stream, "dq")
+    dk = _buffer(dk, q, k.shape, bf16, stream, "dk")
+    dv = _buffer(dv, q, k.shape, bf16, stream, "dv")
+    need = attn_bwd_window_sinks_workspace_size(B, Hq, Hkv, Sq, Sk, d, window, sinks)
+    ws, ws_bytes, workspace = _workspace(workspace, q, need, stream)
+    _launch("attn_bwd_window_sinks", index, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
+            lse.data_ptr(), d_o.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, Hq,
+            Hkv, Sq, Sk, d, float(scale), _addr(k_lens),
+            int(window), int(sinks), ws, ws_bytes, raw)
+    return dq, dk, dv
+
+
+def attn_fwd_paged_window(q, k_cache, v_cache, block_table, cu_seqlens_q, seq_lens_k,
+                          max_seqlen_q: int, scale: float, window: int, sinks: int = 0, out=None,
+                          lse=None, workspace=None, return_lse: bool = True, stream=None):
+    """attn_fwd_paged (causal) with a sliding window (0: none) and the first ``sinks`` tokens
+    visible throughout; returns O [total_q, Hq, d], LSE [Hq, total_q]."""
+    import torch
+    bf16 = torch.bfloat16
+    index = _device_index(q, k_cache, v_cache, block_table, cu_seqlens_q, seq_lens_k, out, lse,
+                          workspace)
+    raw = _raw_stream(stream, index)
+    qs, cache, table = q.shape, k_cache.shape, block_table.shape
+    if len(qs) != 3 or len(cache) != 4 or v_cache.shape != cache or cache[3] != qs[2]:
+        raise ValueError("q [total_q, Hq, d]; caches [num_pages, page_size, Hkv, d]")
+    for t in (q, k_cache, v_cache):
+        if t.dtype is not bf16 or not t.is_contiguous():
+            raise ValueError("q and the caches must be contiguous bfloat16")
+    if len(table) != 2 or block_table.dtype is not torch.int32 or not block_table.is_contiguous():
+        raise ValueError("block_table must be contiguous int32 [B, max_pages_per_seq]")
+    B = table[0]
+    _int32(cu_seqlens_q, (B + 1,), "cu_seqlens_q")
+    _int32(seq_lens_k, (B,), "seq_lens_k")
+    total, Hq, d = qs
+    out = _buffer(out, q, qs, bf16, stream, "out")
+    if lse is not None or return_lse:
+        lse = _buffer(lse, q, (Hq, total), torch.float32, stream, "lse")
+    need = attn_fwd_varlen_workspace_size(B, total, max_seqlen_q)
+    ws, ws_bytes, workspace = _workspace(workspace, q, need, stream)
+    _launch("attn_fwd_paged_window", index, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+            block_table.data_ptr(), cu_seqlens_q.data_ptr(), seq_lens_k.data_ptr(), cache[1], B,
+            Hq, cache[2], total, max_seqlen_q, table[1], cache[0], d,
+            float(scale), int(window), int(sinks), out.data_ptr(), _addr(lse), ws, ws_bytes, raw)
+    return out, lse
 
 
 def attn_get_device_error(stream=None):

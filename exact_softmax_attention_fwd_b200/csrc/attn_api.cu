@@ -3,6 +3,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdint>
@@ -264,7 +265,7 @@ long long varlen_max_units(int B, long long total_q) { return total_q / 256 + B 
 int prefill_dense(const void* q, const void* k, const void* v, void* o, float* lse, int B, int Hq,
                   int Hkv, int Sq, int Sk, int d, int causal, float scale, const int32_t* k_lens,
                   int window, int prefix, const uint8_t* block_mask, int mask_heads,
-                  cudaStream_t stream) {
+                  cudaStream_t stream, int sinks = 0) {
   const long long rows_q = (long long)B * Hq * Sq;
   if (Sk == 0) {
     const size_t n_vec = (size_t)rows_q * d * 2 / 16;
@@ -298,6 +299,7 @@ int prefill_dense(const void* q, const void* k, const void* v, void* o, float* l
   prm.head_pairs = (Hq / Hkv) % 2 == 0 && (window > 0 || block_mask != nullptr) ? 1 : 0;
   prm.window = window;
   prm.prefix = prefix;
+  prm.sinks = window > 0 ? sinks : 0;  // without a window every key is visible as it is
   prm.block_mask = block_mask;
   prm.mask_heads = mask_heads;
   prm.n_qt = (Sq + 127) / 128;
@@ -328,7 +330,8 @@ int launch_bwd(const CUtensorMap& mq, const CUtensorMap& mdo, const CUtensorMap&
   using C = BwdCfg<D>;
   const long long prep_threads = (long long)prm.B * prm.Hq * prm.Sq_pad * (D / 8);
   const long long prep_blocks = (prep_threads + 255) / 256;
-  const long long kv_units = (long long)prm.n_kt * prm.B * prm.Hkv;
+  const long long kv_units =
+      ((long long)prm.n_kt + (long long)prm.far_tiles * prm.far_chunks) * prm.B * prm.Hkv;
   const long long q_units = (long long)prm.n_qt * prm.B * prm.Hq;
   if (prep_blocks > INT_MAX || kv_units > INT_MAX || q_units > INT_MAX) return ATTN_ERR_INVALID_ARG;
   attn_bwd_prep_kernel<D, VARLEN><<<(unsigned)prep_blocks, 256, 0, stream>>>(prm);
@@ -357,6 +360,10 @@ int launch_bwd(const CUtensorMap& mq, const CUtensorMap& mdo, const CUtensorMap&
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, dq, mq, mdo, mk, mv, prm) != cudaSuccess) return ATTN_ERR_CUDA;
+  if (MASKS && prm.far_chunks > 0) {
+    const size_t quads = (size_t)prm.B * prm.Hkv * prm.far_rows * 2 * D / 4;
+    attn_bwd_far_join_kernel<D><<<(unsigned)((quads + 255) / 256), 256, 0, stream>>>(prm);
+  }
   return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
@@ -500,7 +507,7 @@ int paged_prefill_run(const void* q, const void* k_cache, const void* v_cache,
                       const int32_t* seq_lens_k, int page_size, int B, int Hq, int Hkv,
                       long long total_q, int max_seqlen_q, int max_pages_per_seq, int num_pages,
                       int d, int causal, float scale, void* o, float* lse, void* workspace,
-                      cudaStream_t stream) {
+                      cudaStream_t stream, int window = 0, int sinks = 0) {
   int* unit_count = static_cast<int*>(workspace);
   int2* units = reinterpret_cast<int2*>(static_cast<char*>(workspace) + 16);
   const long long max_units = varlen_max_units(B, total_q);
@@ -511,7 +518,7 @@ int paged_prefill_run(const void* q, const void* k_cache, const void* v_cache,
   if (!schedule_smem_ready()) return ATTN_ERR_CUDA;
   attn_varlen_schedule_kernel<<<1, 1024, sched_smem, stream>>>(
       cu_seqlens_q, nullptr, seq_lens_k, B, (int)total_q, 0, max_seqlen_q, max_keys, causal,
-      0, 0, shift, n_levels, units, unit_count, (int)max_units);
+      window, 0, shift, n_levels, units, unit_count, (int)max_units);
   if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
   CUtensorMap mq, mk, mv;
   if (!make_token_map(&mq, q, d, Hq, total_q) ||
@@ -536,6 +543,14 @@ int paged_prefill_run(const void* q, const void* k_cache, const void* v_cache,
   prm.units = units;
   prm.unit_count = unit_count;
   prm.total_q = (int)total_q;
+  if (window > 0) {  // causal
+    prm.window = window;
+    prm.sinks = sinks;
+    prm.v_pool = static_cast<const uint16_t*>(v_cache);
+    return d == 128
+               ? launch_prefill<128, true, kLayoutPaged, true>(mq, mk, mv, mq, prm, stream, max_units)
+               : launch_prefill<64, true, kLayoutPaged, true>(mq, mk, mv, mq, prm, stream, max_units);
+  }
   if (d == 128)
     return causal ? launch_prefill<128, true, kLayoutPaged>(mq, mk, mv, mq, prm, stream, max_units)
                   : launch_prefill<128, false, kLayoutPaged>(mq, mk, mv, mq, prm, stream, max_units);
@@ -738,6 +753,36 @@ size_t bwd_workspace_bytes(int B, int Hq, int Sq) {
   const size_t pad = ((size_t)Sq + 127) / 128 * 128;
   return 2 * (size_t)B * Hq * pad * sizeof(float);
 }
+
+// How the first tokens' far query tiles (those that see a key tile through its
+// first tokens alone) are dealt to units of the dK/dV kernel: chunks per key
+// tile, as long as an ordinary unit (the window's query tiles of the group),
+// but no more units than four for every SM, which also bounds the partial
+// sums' memory.  0 chunks: no query tile is far.
+struct BwdFar {
+  int tiles, chunks, rows;
+  size_t bytes;  // of partial sums
+};
+
+BwdFar bwd_far(int B, int Hq, int Hkv, int Sq, int Sk, int d, int window, int sinks) {
+  BwdFar f = {0, 0, 0, 0};
+  if (window <= 0 || sinks <= 0 || Sk <= 0) return f;
+  const long long n_qt = ((long long)Sq + 127) / 128;
+  // the first row past the window of key tile 0, for a whole key length (a
+  // shorter one moves it back further than the tile's last key)
+  const long long row_end = std::min(127, Sk - 1) + (long long)window - ((long long)Sk - Sq);
+  const long long near_qt = row_end <= 0 ? 0 : (row_end + 127) / 128;
+  if (near_qt >= n_qt) return f;
+  const long long group = Hq / Hkv, bh = (long long)B * Hkv;
+  f.rows = std::min(sinks, Sk);
+  f.tiles = (f.rows + 127) / 128;
+  const long long unit = group * ((long long)window / 128 + 2);
+  const long long by_length = (group * (n_qt - near_qt) + unit - 1) / unit;
+  const long long by_count = std::max(1ll, 4 * 148 / (f.tiles * bh));
+  f.chunks = (int)std::min(by_length, by_count);
+  f.bytes = (size_t)(f.chunks + 1) * bh * f.rows * 2 * d * sizeof(float);
+  return f;
+}
 }  // namespace
 }  // namespace attn_b200
 
@@ -760,7 +805,7 @@ int bwd_dense(const void* q, const void* k, const void* v, const void* o, const 
               const void* d_o, void* dq, void* dk, void* dv, int B, int Hq, int Hkv, int Sq, int Sk,
               int d, int causal, float scale, const int32_t* k_lens, int window, int prefix,
               const uint8_t* block_mask, int mask_heads, void* workspace, size_t workspace_bytes,
-              attn_stream_t stream_) {
+              attn_stream_t stream_, int sinks = 0) {
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
   if (o == nullptr || lse == nullptr || d_o == nullptr || dq == nullptr || workspace == nullptr ||
       (Sk > 0 && (dk == nullptr || dv == nullptr)))
@@ -770,7 +815,9 @@ int bwd_dense(const void* q, const void* k, const void* v, const void* o, const 
   if (!aligned16(o) || !aligned16(d_o) || !aligned16(workspace) || !aligned4(lse) ||
       (Sk > 0 && (!aligned16(dk) || !aligned16(dv))))
     return ATTN_ERR_ALIGNMENT;
-  if (workspace_bytes < bwd_workspace_bytes(B, Hq, Sq)) return ATTN_ERR_WORKSPACE;
+  const size_t stat_bytes = bwd_workspace_bytes(B, Hq, Sq);
+  const BwdFar far = bwd_far(B, Hq, Hkv, Sq, Sk, d, window, sinks);
+  if (workspace_bytes < stat_bytes + far.bytes) return ATTN_ERR_WORKSPACE;
   if (Sk == 0) {  // no key: every output row is constant zero, so dQ = 0 (dK, dV are empty)
     const size_t bytes = (size_t)B * Hq * Sq * d * 2;
     return cudaMemsetAsync(dq, 0, bytes, stream) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
@@ -807,6 +854,11 @@ int bwd_dense(const void* q, const void* k, const void* v, const void* o, const 
   prm.prefix = prefix;
   prm.block_mask = block_mask;
   prm.mask_heads = mask_heads;
+  prm.sinks = window > 0 ? sinks : 0;
+  prm.far_tiles = far.tiles;
+  prm.far_chunks = far.chunks;
+  prm.far_rows = far.rows;
+  prm.far_part = reinterpret_cast<float*>(static_cast<char*>(workspace) + stat_bytes);
   if (window > 0 || prefix > 0 || block_mask != nullptr) {
     if (d == 128)
       return causal ? launch_bwd<128, true, false, true>(mq, mdo, mk, mv, prm, stream)
@@ -1297,3 +1349,4 @@ extern "C" int attn_decode_paged_noalloc(const void* q, const void* k_cache, con
 }
 
 #include "rope_api.cuh"
+#include "window_api.cuh"

@@ -78,6 +78,16 @@ struct BwdParams {
   int window, prefix;
   const uint8_t* block_mask;
   int mask_heads;
+  // visible first tokens (with a window): keys below `sinks` are seen by every
+  // row at or past them.  Their dK, dV gather from all later query tiles, so
+  // the tiles behind the window are dealt to `far_chunks` units of their own
+  // per key tile that holds first tokens (far_tiles of them); far_chunks 0:
+  // no such units, and the key tile's one unit walks all of it
+  int sinks, far_tiles, far_chunks;
+  // fp32 partial sums of the first tokens' dK and dV: [far_chunks + 1, B * Hkv,
+  // far_rows, 2, d], slot 0 from the key tile's own unit (far_chunks > 0)
+  float* far_part;
+  int far_rows;         // min(sinks, Sk)
 };
 
 // Whether the 128 x 128 block (query tile qt, key tile kt) of query head hq is
@@ -332,9 +342,15 @@ __global__ void __launch_bounds__(384, 1)
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
 
-  // ---- the unit and its query-tile range
-  const int bh_kv = blockIdx.x % (p.B * p.Hkv);
-  const int kb = blockIdx.x / (p.B * p.Hkv);
+  // ---- the unit and its query-tile range.  Units of first tokens' far query
+  // tiles come first (they are at least as long as the others).
+  const int BH = p.B * p.Hkv;
+  const int n_far = MASKS ? p.far_tiles * p.far_chunks : 0;
+  const int unit = blockIdx.x / BH;
+  const bool far = MASKS && unit < n_far;
+  const int bh_kv = blockIdx.x % BH;
+  const int kb = far ? unit / p.far_chunks : unit - n_far;
+  const int slot = far ? unit % p.far_chunks + 1 : 0;  // its slot of partial sums
   const int b = bh_kv / p.Hkv, kvh = bh_kv % p.Hkv;
   BwdSeq sq;
   const bool seq_ok = bwd_sequence<VARLEN>(p, b, threadIdx.x == 0 && kb == 0 && kvh == 0, sq);
@@ -355,10 +371,22 @@ __global__ void __launch_bounds__(384, 1)
     if (p.window > 0) {
       const long long row_end = key1 + p.window - koff;
       qt_hi = row_end <= 0 ? 0 : (int)min((row_end + 127) / 128, (long long)n_qt);
+      if (far) {  // what the window leaves of the rows that see the tile's first tokens
+        qt_lo = max(qt_lo, qt_hi);
+        qt_hi = n_qt;
+      } else if (key0 < p.sinks && p.far_chunks == 0) {
+        qt_hi = n_qt;
+      }
     }
   }
   const int nq = (!seq_ok || key0 >= klen || qt_hi <= qt_lo) ? 0 : qt_hi - qt_lo;
-  const int N = p.group * nq;  // (query head, query tile) candidates
+  // (query head, query tile) candidates; a far unit takes its share [c_lo, c_lo + N)
+  int N = p.group * nq, c_lo = 0;
+  if (far) {
+    const long long all = N;
+    c_lo = (int)(all * (slot - 1) / p.far_chunks);
+    N = (int)(all * slot / p.far_chunks) - c_lo;
+  }
   // with a block mask, only the candidates whose block is on are walked
   const bool listed = MASKS && p.block_mask != nullptr && N > 0 && N <= C::LIST_MAX;
   const uint16_t* list = reinterpret_cast<const uint16_t*>(sbase_ptr + C::KV_OFF_LIST);
@@ -397,7 +425,7 @@ __global__ void __launch_bounds__(384, 1)
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
   const int NI = listed ? *list_count : N;  // iterations walked
-  auto cand = [&](int n) { return listed ? (int)list[n] : n; };
+  auto cand = [&](int n) { return listed ? (int)list[n] : n + c_lo; };
   const uint32_t sK = sbase + C::KV_OFF_K, sV = sbase + C::KV_OFF_V;
   auto sQ = [&](int s) { return sbase + C::KV_OFF_Q + (uint32_t)s * C::TILE_BYTES; };
   auto sDO = [&](int s) { return sbase + C::KV_OFF_DO + (uint32_t)s * C::TILE_BYTES; };
@@ -506,7 +534,8 @@ __global__ void __launch_bounds__(384, 1)
       long long cm = (j >= klen) ? 64 : (CAUSAL ? (long long)j - koff - qt * 128 - c0 : 0);
       long long cx = 64;  // columns [cmin, cmax) are visible to this key
       if (MASKS) {
-        if (p.window > 0 && j < klen) cx = (long long)j + p.window - koff - qt * 128 - c0;
+        if (p.window > 0 && j < klen && j >= p.sinks)
+          cx = (long long)j + p.window - koff - qt * 128 - c0;
         if (p.prefix > 0 && j < p.prefix && j < klen) {
           cm = 0;
           cx = 64;
@@ -603,6 +632,11 @@ __global__ void __launch_bounds__(384, 1)
     if ((!have || ok) && key0 < key_rows) {
       const uint32_t t_acc = tmem + lane_off + (wg ? C::KV_TM_DK : C::KV_TM_DV);
       const int jj = j < key_rows ? j : 0;
+      // first tokens whose sum is shared by several units: fp32 partials
+      const bool shared_row = MASKS && p.far_chunks > 0 && j < p.far_rows;
+      float* part = nullptr;
+      if (MASKS && shared_row)
+        part = p.far_part + ((((size_t)slot * BH + bh_kv) * p.far_rows + j) * 2 + wg) * D;
       uint16_t* out = (wg ? p.dk : p.dv) +
                       (VARLEN ? ((size_t)(sq.k0 + jj) * p.Hkv + kvh) : ((size_t)bh_kv * p.Sk + jj)) * D;
       const float mul = wg ? p.scale : 1.f;
@@ -615,7 +649,15 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
           for (int e = 0; e < 32; ++e) v[e] = 0u;
         }
-        if (j < key_rows) bwd_store32(out + c, v, mul);
+        if (MASKS && shared_row) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<float4*>(part + c + e) =
+                make_float4(__uint_as_float(v[e]), __uint_as_float(v[e + 1]),
+                            __uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]));
+        } else if (j < key_rows && !far) {
+          bwd_store32(out + c, v, mul);
+        }
       }
     }
   }
@@ -624,6 +666,34 @@ __global__ void __launch_bounds__(384, 1)
   __syncthreads();
   tc_fence_after_sync();
   if (warp == 1) tmem_dealloc(tmem, C::TMEM_COLS);
+}
+
+// The shared dK, dV rows of the first tokens: the partial sums of all their
+// units, added in a fixed order in fp32, scaled and rounded once.  One thread
+// per 4 elements.
+template <int D>
+__global__ void __launch_bounds__(256) attn_bwd_far_join_kernel(const BwdParams p) {
+  const size_t rows = (size_t)p.B * p.Hkv * p.far_rows;
+  const size_t at = ((size_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (at >= rows * 2 * D) return;
+  const size_t stride = rows * 2 * D;
+  float4 sum = *reinterpret_cast<const float4*>(p.far_part + at);
+  for (int c = 1; c <= p.far_chunks; ++c) {
+    const float4 x = *reinterpret_cast<const float4*>(p.far_part + c * stride + at);
+    sum.x += x.x;
+    sum.y += x.y;
+    sum.z += x.z;
+    sum.w += x.w;
+  }
+  const size_t row = at / (2 * D);
+  const int e = (int)(at % (2 * D));
+  const bool is_k = e >= D;
+  const float mul = is_k ? p.scale : 1.f;
+  const size_t bh = row / p.far_rows, j = row % p.far_rows;
+  uint2 w;
+  w.x = pack_bf16x2(sum.x * mul, sum.y * mul);
+  w.y = pack_bf16x2(sum.z * mul, sum.w * mul);
+  *reinterpret_cast<uint2*>((is_k ? p.dk : p.dv) + (bh * p.Sk + j) * D + (is_k ? e - D : e)) = w;
 }
 
 // ===========================================================================
@@ -671,7 +741,13 @@ __global__ void __launch_bounds__(384, 1)
   }
   // key tiles [kt_lo, kt_lo + N); none for a tile past the sequence's rows
   const int kt_end = max_key < 0 ? 0 : (int)(max_key / 128) + 1;
-  const int N = (row0 >= n_rows || kt_end <= kt_lo) ? 0 : kt_end - kt_lo;
+  // the tiles of visible first tokens, when the window leaves a gap behind them
+  int st = 0;
+  if (MASKS && p.sinks > 0) {
+    st = (min(p.sinks, klen) + 127) / 128;
+    if (kt_lo <= st) kt_lo = st = 0;
+  }
+  const int N = (row0 >= n_rows || kt_end <= kt_lo) ? 0 : st + kt_end - kt_lo;
   // with a block mask, only the key tiles whose block is on are walked
   const bool listed = MASKS && p.block_mask != nullptr && N > 0 && N <= C::LIST_MAX;
   const uint16_t* list = reinterpret_cast<const uint16_t*>(sbase_ptr + C::Q_OFF_LIST);
@@ -706,7 +782,10 @@ __global__ void __launch_bounds__(384, 1)
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
   const int NI = listed ? *list_count : N;  // key tiles walked
-  auto cand = [&](int n) { return listed ? (int)list[n] : n; };
+  // the n-th key tile walked
+  auto key_tile = [&](int n) {
+    return listed ? kt_lo + (int)list[n] : (MASKS && n < st) ? n : kt_lo + n - (MASKS ? st : 0);
+  };
   const uint32_t sQ = sbase + C::Q_OFF_Q, sDO = sbase + C::Q_OFF_DO;
   auto sK = [&](int s) { return sbase + C::Q_OFF_K + (uint32_t)s * C::TILE_BYTES; };
   auto sV = [&](int s) { return sbase + C::Q_OFF_V + (uint32_t)s * C::TILE_BYTES; };
@@ -733,7 +812,7 @@ __global__ void __launch_bounds__(384, 1)
             !(ok = mbar_wait(bar(C::QB_KVE + s), ((n / C::STAGES) - 1) & 1u, abort_flag)))
           break;
         mbar_arrive_expect_tx(bar(C::QB_KVF + s), 2 * C::TILE_BYTES);
-        const int kt = kt_lo + cand(n);
+        const int kt = key_tile(n);
         const int ky = VARLEN ? kvh : kt * 128, kz = VARLEN ? sq.k0 + kt * 128 : bh_kv;
         for (int cb = 0; cb < C::NCB; ++cb) {
           tma_load_3d(sK(s) + cb * C::CB_BYTES, &tm_k, bar(C::QB_KVF + s), 64 * cb, ky, kz);
@@ -800,13 +879,16 @@ __global__ void __launch_bounds__(384, 1)
     if (MASKS && p.window > 0) klo = max(0LL, (long long)row + koff - p.window + 1);
     bool ok = true;
     for (int n = 0; ok && n < NI; ++n) {
-      const int kt = kt_lo + cand(n);
+      const int kt = key_tile(n);
       const long long t0 = (long long)kt * 128 + c0;  // this run's first key
       long long cm = kend - t0;  // visible iff cmin <= c < cmax
       if (MASKS && !bwd_block_on(p, b, hq, qt, kt)) cm = 0;
       const long long cn = MASKS ? klo - t0 : 0;
       const int cmin = (int)(cn < 0 ? 0 : (cn > 64 ? 64 : cn));
       const int cmax = (int)(cm < 0 ? 0 : (cm > 64 ? 64 : cm));
+      // columns below csink are first tokens, visible below cmin too
+      const long long cs = MASKS ? (long long)p.sinks - t0 : 0;
+      const int csink = MASKS ? (int)(cs < 0 ? 0 : (cs > 64 ? 64 : cs)) : 0;
       const bool edge = __any_sync(0xffffffffu, cmax < 64 || cmin > 0);
       if (!(ok = mbar_wait_warp(bar(C::QB_SF + (n & 1)), (n >> 1) & 1u, abort_flag))) break;
       tc_fence_after_sync();
@@ -827,8 +909,8 @@ __global__ void __launch_bounds__(384, 1)
           split_f32x2(fma_f32x2(f32x2(__uint_as_float(s0), __uint_as_float(s1)), c2x2, nlx2), x0,
                       x1);
           if (edge) {
-            x0 = bwd_keep(c < cmax && c >= cmin, x0);
-            x1 = bwd_keep(c + 1 < cmax && c + 1 >= cmin, x1);
+            x0 = bwd_keep(c < cmax && (c >= cmin || (MASKS && c < csink)), x0);
+            x1 = bwd_keep(c + 1 < cmax && (c + 1 >= cmin || (MASKS && c + 1 < csink)), x1);
           }
           pr[c] = ex2(x0);
           pr[c + 1] = ex2(x1);

@@ -82,6 +82,8 @@ struct PrefillParams {
   // programmable masks (causal only; 0 = off): a row at key position p sees
   // keys (p - window, p] (sliding window), or keys below prefix as well (prefix-LM)
   int window, prefix;
+  // with a window: keys below `sinks` stay visible to every row at or past them
+  int sinks;
   // block-sparse mask (MASKS instantiations; nullable): uint8 [B, mask_heads,
   // n_qt, n_kt] over 128 x 128 (query tile, key tile) blocks, 0 = skipped
   const uint8_t* block_mask;
@@ -99,6 +101,7 @@ struct PrefillParams {
   const int* seq_lens_k;    // [B] keys of each sequence
   const int* block_table;   // [B, max_pages]
   int max_pages, page_size, num_pages;
+  const uint16_t* v_pool;   // the V pool itself (masked paged launches: tail pages)
   const int2* units;    // (sequence, query block), heaviest first
   const int* unit_count;
   int total_q;
@@ -210,6 +213,13 @@ struct PrefillUnit {
   int kv_end[2];
   int kv_first;    // the unit's K/V stream: tiles [kv_first, kv_last)
   int kv_last;
+  // With visible first tokens behind which the window leaves a gap, the stream
+  // is the tiles of those tokens, then the window's: stream position x is key
+  // tile x below `sink_tiles` and x + `gap` from there on, and kv_begin,
+  // kv_end, kv_first, kv_last above are stream positions.  Otherwise both are 0
+  // and stream positions are key tiles.
+  int sink_tiles, gap;
+  __device__ __forceinline__ int key_tile(int x) const { return x < sink_tiles ? x : x + gap; }
 };
 
 // The k-th unit of this CTA, or false when the CTA has no more work.  Ranks
@@ -309,6 +319,26 @@ __device__ __forceinline__ bool prefill_unit(const PrefillParams& p, int k, Pref
     }
   }
   if (u.kv_last == 0) u.kv_first = 0;
+  u.sink_tiles = u.gap = 0;
+  if (MASKS && p.sinks > 0 && u.kv_last > 0) {
+    // Both query tiles walk the whole stream from its start: where their
+    // windows begin a tile apart, the later one meets one tile that it does
+    // not see (masked element by element), which keeps their runs contiguous.
+    const int st = (min(p.sinks, u.klen) + 127) / 128;  // tiles that hold first tokens
+    if (u.kv_first > st) {
+      u.sink_tiles = st;
+      u.gap = u.kv_first - st;
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (u.kv_end[i] > u.kv_begin[i]) {
+        u.kv_begin[i] = 0;
+        u.kv_end[i] -= u.gap;
+      }
+    }
+    u.kv_first = 0;
+    u.kv_last -= u.gap;
+  }
   return true;
 }
 
@@ -452,12 +482,13 @@ __global__ void __launch_bounds__(384, 1)
             continue;
           const int s = kv % C::STAGES;
           const uint32_t ph = (kv / C::STAGES) & 1u;
+          const int key0 = (MASKS ? u.key_tile(j) : j) * 128;
           if (!(ok = mbar_wait(bar(C::B_KEMPTY + s), ph ^ 1u, abort_flag))) break;
           mbar_arrive_expect_tx(bar(C::B_KFULL + s), C::TILE_BYTES);
           for (int cb = 0; cb < C::NCB; ++cb)
             tma_load_3d(sbase + C::OFF_K + s * C::TILE_BYTES + cb * C::CB_BYTES, &tm_k,
-                        bar(C::B_KFULL + s), 64 * cb, VARLEN ? kvh : j * 128,
-                        VARLEN ? u.k_tok0 + j * 128 : kv_row);
+                        bar(C::B_KFULL + s), 64 * cb, VARLEN ? kvh : key0,
+                        VARLEN ? u.k_tok0 + key0 : kv_row);
           if (j == u.kv_first && has1 && !(ok = load_q(u, 1))) {
             ++kv;  // K_0 of this unit was issued
             break;
@@ -469,8 +500,8 @@ __global__ void __launch_bounds__(384, 1)
           mbar_arrive_expect_tx(bar(C::B_VFULL + s), C::TILE_BYTES);
           for (int cb = 0; cb < C::NCB; ++cb)
             tma_load_3d(sbase + C::OFF_V + s * C::TILE_BYTES + cb * C::CB_BYTES, &tm_v,
-                        bar(C::B_VFULL + s), 64 * cb, VARLEN ? kvh : j * 128,
-                        VARLEN ? u.k_tok0 + j * 128 : kv_row);
+                        bar(C::B_VFULL + s), 64 * cb, VARLEN ? kvh : key0,
+                        VARLEN ? u.k_tok0 + key0 : kv_row);
           ++kv;
         }
       }
@@ -507,12 +538,17 @@ __global__ void __launch_bounds__(384, 1)
       for (int j = u.kv_first; j < u.kv_last; ++j, ++kv) {
         const int s = kv % C::STAGES;
         const uint32_t ph = (kv / C::STAGES) & 1u;
-        const int lp = j * ppt + lane;
+        const int tile = MASKS ? u.key_tile(j) : j;
+        const int lp = tile * ppt + lane;
         const int phys = (lane < ppt && lp < n_lp) ? __ldg(tbl + lp) : kNoPage;
         const bool valid = phys >= 0 && phys < p.num_pages;
         if (phys != kNoPage && !valid) flag_device_error(kDevErrBadPage);  // skipped: its
         const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, valid)) *  // keys read
                                (uint32_t)(p.page_size * 128 * C::NCB);  // as earlier finite rows
+        // a last page that its sequence does not fill: see below
+        const uint32_t tails =
+            MASKS ? __ballot_sync(0xffffffffu, valid && (long long)(lp + 1) * p.page_size > u.klen)
+                  : 0u;
         if (!(ok = mbar_wait_warp(bar(C::B_KEMPTY + s), ph ^ 1u, abort_flag))) break;
         if (lane == 0) mbar_arrive_expect_tx(bar(C::B_KFULL + s), bytes);
         __syncwarp();
@@ -524,9 +560,32 @@ __global__ void __launch_bounds__(384, 1)
           ++kv;  // K of this tile was issued
           break;
         }
-        if (lane == 0) mbar_arrive_expect_tx(bar(C::B_VFULL + s), bytes);
+        uint32_t v_bytes = bytes;
+        if (MASKS && tails != 0) {
+          // The rows behind the sequence's end may never have been written and
+          // hold anything: their weights are 0, but 0 * NaN is not.  The
+          // warp copies the rows in use itself, so that the others keep what
+          // the ring held before (zeros or earlier rows in use).  K needs no
+          // such care: a K row reaches its own score column alone.
+          const int from = __ffs(tails) - 1;
+          const int r0 = from * p.page_size;  // its first row in the tile
+          const int rows = u.klen - (tile * 128 + r0);
+          const size_t tok = (size_t)__shfl_sync(0xffffffffu, phys, from) * p.page_size;
+          uint8_t* dst = sbase_ptr + C::OFF_V + s * C::TILE_BYTES;
+          for (int x = lane; x < rows * (D / 8); x += 32) {
+            const int r = r0 + x / (D / 8), ch = x % (D / 8);
+            const uint4 w = *reinterpret_cast<const uint4*>(
+                p.v_pool + ((tok + (size_t)(r - r0)) * p.Hkv + kvh) * D + 8 * ch);
+            *reinterpret_cast<uint4*>(dst + (ch >> 3) * C::CB_BYTES + r * 128 +
+                                      (((ch & 7) ^ (r & 7)) << 4)) = w;
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          v_bytes -= (uint32_t)(p.page_size * 128 * C::NCB);
+        }
+        if (lane == 0) mbar_arrive_expect_tx(bar(C::B_VFULL + s), v_bytes);
         __syncwarp();
-        if (valid)
+        if (valid && !(MASKS && ((tails >> lane) & 1u)))
           for (int cb = 0; cb < C::NCB; ++cb)
             tma_load_3d(sbase + C::OFF_V + s * C::TILE_BYTES + cb * C::CB_BYTES + row_off, &tm_v,
                         bar(C::B_VFULL + s), 64 * cb, kvh, phys * p.page_size);
@@ -806,15 +865,24 @@ __global__ void __launch_bounds__(384, 1)
             s[96 + e] = __uint_as_float(u3[e]);
           }
         }
-        if ((long long)j * 128 + 127 > hi_tile || (MASKS && (long long)j * 128 < lo_tile)) {
+        const long long key0 = (long long)(MASKS ? u.key_tile(j) : j) * 128;
+        if (key0 + 127 > hi_tile || (MASKS && key0 < lo_tile)) {
           // boundary tile: per-element predicate, in 32-bit once clamped to the tile
-          const long long hl = hi_row - (long long)j * 128;
-          const long long ll = lo_row - (long long)j * 128;
+          const long long hl = hi_row - key0;
+          const long long ll = lo_row - key0;
           const int hi_local = hl < -1 ? -1 : (hl > 127 ? 127 : (int)hl);
           const int lo_local = ll < 0 ? 0 : (ll > 128 ? 128 : (int)ll);
+          if (MASKS && p.sinks > key0) {
+            // columns below sk are first tokens: hidden are [sk, lo_local) and past hi_local
+            const int sk = (int)min((long long)p.sinks - key0, 128LL);
 #pragma unroll
-          for (int c = 0; c < 128; ++c)
-            if (c > hi_local || (MASKS && c < lo_local)) s[c] = -INFINITY;
+            for (int c = 0; c < 128; ++c)
+              if (c > hi_local || (c < lo_local && c >= sk)) s[c] = -INFINITY;
+          } else {
+#pragma unroll
+            for (int c = 0; c < 128; ++c)
+              if (c > hi_local || (MASKS && c < lo_local)) s[c] = -INFINITY;
+          }
         }
         if (!scale_pos) {
 #pragma unroll

@@ -661,6 +661,66 @@ int attn_append_paged_fp8(const void* q, const void* k, const void* v, void* q_o
                           int rotary_dim, int interleaved, float mscale, const long long* strides,
                           attn_stream_t stream);
 
+/*
+ * attn_fwd_window_sinks -- attn_fwd_window's sliding window, with the first
+ * `sinks` tokens staying visible.
+ *   A query row at key position p = i + (k_len[b] - Sq) sees key j iff j <= p,
+ *   j < k_len[b] and (j > p - window or j < sinks).  window = 0: no window
+ *   (attn_fwd_masked with causal = 1; sinks then change nothing); sinks = 0:
+ *   attn_fwd_window.  Both may exceed the sequence.
+ *   Key tiles between the first tokens and a row block's window are skipped.
+ *   Keys and values of the whole [B, Hkv, Sk, d] tensors, padding included,
+ *   must be finite (a padded row has weight 0, and 0 * NaN is not 0).
+ * Other arguments, layouts and errors as attn_fwd_masked (INVALID_ARG also for
+ * a negative window or sinks).
+ */
+int attn_fwd_window_sinks(const void* q, const void* k, const void* v, void* o, float* lse, int B,
+                          int Hq, int Hkv, int Sq, int Sk, int d, float scale,
+                          const int32_t* k_lens, int window, int sinks, attn_stream_t stream);
+
+/*
+ * attn_fwd_paged_window -- attn_fwd_paged (causal) with a sliding window and
+ * visible first tokens, masked as attn_fwd_window_sinks with k_len =
+ * seq_lens_k[b] and Sq the sequence's query tokens.  Pages that lie wholly
+ * between the first tokens and the windows of a block of query rows are not
+ * read.  Slots behind a sequence's end may hold anything (a cache whose last
+ * page was never filled); the slots in use must be finite.
+ * Other arguments, layouts, workspace, device-side checks and errors as
+ * attn_fwd_paged (INVALID_ARG also for a negative window or sinks).
+ */
+int attn_fwd_paged_window(const void* q, const void* k_cache, const void* v_cache,
+                          const int32_t* block_table, const int32_t* cu_seqlens_q,
+                          const int32_t* seq_lens_k, int page_size, int B, int Hq, int Hkv,
+                          long long total_q, int max_seqlen_q, int max_pages_per_seq,
+                          int num_pages, int d, float scale, int window, int sinks, void* o,
+                          float* lse, void* workspace, size_t workspace_bytes,
+                          attn_stream_t stream);
+
+/*
+ * attn_bwd_window_sinks_workspace_size -- bytes of device workspace
+ * attn_bwd_window_sinks needs: attn_bwd_workspace_size's row statistics, and
+ * fp32 partial sums of the first tokens' dK and dV, which gather from every
+ * later query row and are therefore summed by several CTAs (none when the
+ * window reaches all rows).  0 for invalid arguments.
+ */
+size_t attn_bwd_window_sinks_workspace_size(int B, int Hq, int Hkv, int Sq, int Sk, int d,
+                                            int window, int sinks);
+
+/*
+ * attn_bwd_window_sinks -- backward pass of attn_fwd_window_sinks.
+ *   Arguments and layouts as attn_bwd (causal implied); window and sinks
+ *   exactly as given to the forward; workspace of
+ *   attn_bwd_window_sinks_workspace_size(...) bytes.  Every element of dq, dk
+ *   and dv is written.  Deterministic: partial sums are added in a fixed order,
+ *   without atomics.  q, k, v, o and d_o, padding included, must be finite.
+ * Errors: as attn_bwd, plus INVALID_ARG for a negative window or sinks.
+ */
+int attn_bwd_window_sinks(const void* q, const void* k, const void* v, const void* o,
+                          const float* lse, const void* d_o, void* dq, void* dk, void* dv, int B,
+                          int Hq, int Hkv, int Sq, int Sk, int d, float scale,
+                          const int32_t* k_lens, int window, int sinks, void* workspace,
+                          size_t workspace_bytes, attn_stream_t stream);
+
 /* attn_strerror -- static description of an attn_status value. */
 const char* attn_strerror(int status);
 

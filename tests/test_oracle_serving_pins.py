@@ -105,3 +105,75 @@ def test_frequency_tables():
 def test_frequency_refusals(kw):
     with pytest.raises(ValueError):
         rope_frequencies(**kw)
+
+
+# ------------------------------------------------------------- window with first tokens
+
+def _dense(B=2, Hq=4, Hkv=2, Sq=37, Sk=50, d=16, seed=3):
+    g = np.random.default_rng(seed)
+    # bf16 values, so that the C oracle reads the same numbers
+    as_bf16 = lambda x: torch.tensor(x, dtype=torch.float32).to(torch.bfloat16)  # noqa: E731
+    return (as_bf16(g.standard_normal((B, Hq, Sq, d))), as_bf16(g.standard_normal((B, Hkv, Sk, d))),
+            as_bf16(g.standard_normal((B, Hkv, Sk, d))))
+
+
+def test_window_rule_by_enumeration():
+    seen = S.window_visible([-1, 0, 4, 9], 12, 3, 2)
+    assert [np.flatnonzero(r).tolist() for r in seen] == \
+        [[], [0], [0, 1, 2, 3, 4], [0, 1, 7, 8, 9]]
+    assert S.window_visible([5], 12, 0, 0)[0].tolist() == [True] * 6 + [False] * 6
+    assert S.window_visible([9], 12, 1, 0)[0].nonzero()[0].tolist() == [9]
+
+
+@pytest.mark.parametrize("window", [0, 1, 7, 64])
+def test_without_first_tokens_it_is_the_window_oracle(window):
+    import oracle
+    q, k, v = _dense()
+    lens = torch.tensor([50, 20], dtype=torch.int32)
+    o, lse = S.window_fwd(q, k, v, 0.3, window, 0, lens)
+    ro, rl = oracle.attn_fwd(q, k, v, True, 0.3, k_lens=lens, window=window)
+    np.testing.assert_allclose(o, ro, rtol=0, atol=1e-12)
+    np.testing.assert_allclose(lse, rl, rtol=0, atol=1e-12)
+
+
+def test_enough_first_tokens_are_plain_causal_attention():
+    import oracle
+    q, k, v = _dense()
+    o, lse = S.window_fwd(q, k, v, 0.3, 4, 50)
+    ro, rl = oracle.attn_fwd(q, k, v, True, 0.3)
+    np.testing.assert_allclose(o, ro, rtol=0, atol=1e-12)
+    np.testing.assert_allclose(lse, rl, rtol=0, atol=1e-12)
+
+
+def test_window_gradients_match_differences():
+    q, k, v = (S.f64(x) for x in _dense(1, 2, 1, 9, 12, 4))
+    g = np.random.default_rng(4)
+    do = g.standard_normal(q.shape)
+    lens = [11]
+    grads = S.window_grads(q, k, v, do, 0.5, 3, 2, lens)
+    for which, (x, grad) in enumerate(zip((q, k, v), grads)):
+        for _ in range(25):
+            at = tuple(int(g.integers(n)) for n in x.shape)
+            args = [q, k, v]
+            vals = []
+            for h in (1e-5, -1e-5):
+                y = x.copy()
+                y[at] += h
+                args[which] = y
+                vals.append((S.window_fwd(*args, 0.5, 3, 2, lens)[0] * do).sum())
+            assert abs((vals[0] - vals[1]) / 2e-5 - grad[at]) < 1e-7
+
+
+def test_paged_and_single_token_forms_gather_the_dense_one():
+    q, k, v = (S.f64(x) for x in _dense(1, 4, 2, 5, 40, 8))
+    table = [[2, 0, 1, 3, 4]]
+    kc, vc = np.zeros((5, 8, 2, 8)), np.zeros((5, 8, 2, 8))
+    for t in range(40):
+        kc[table[0][t // 8], t % 8], vc[table[0][t // 8], t % 8] = k[0, :, t], v[0, :, t]
+    o, lse = S.window_fwd(q, k, v, 0.4, 6, 3)
+    po, pl = S.paged_window(q[0].transpose(1, 0, 2), kc, vc, table, [0, 5], [40], 0.4, 6, 3)
+    np.testing.assert_allclose(po.transpose(1, 0, 2), o[0], atol=1e-13)
+    np.testing.assert_allclose(pl, lse[0], atol=1e-13)
+    do, dl = S.paged_window(q[0, :, -1][None], kc, vc, table, None, [40], 0.4, 6, 3)
+    np.testing.assert_allclose(do[0], o[0, :, -1], atol=1e-13)
+    np.testing.assert_allclose(dl[0], lse[0, :, -1], atol=1e-13)
