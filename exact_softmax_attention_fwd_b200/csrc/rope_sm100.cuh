@@ -30,6 +30,7 @@
 namespace attn_b200 {
 
 constexpr int kRopeThreads = 256;
+constexpr int kRopeBatch = 4;  // heads whose rows a thread has in flight
 
 struct RopeParams {
   const uint16_t* q;      // element (b, h, s, :) at b * qs[0] + h * qs[1] + s * qs[2]
@@ -47,6 +48,17 @@ struct RopeParams {
   float mscale, sin_sign;
 };
 
+// A 16-byte load of data that is read once (no L1 line is kept; the line may be
+// written by this kernel, when it works in place, so it is not a read-only load).
+__device__ __forceinline__ uint4 ld_once_v4(const void* p) {
+  uint4 r;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p)
+               : "memory");
+  return r;
+}
+
 // Element offsets of the two 8-element pieces of chunk c of a head row.
 template <bool INTERLEAVED>
 __device__ __forceinline__ void rope_pieces(int c, int rot_chunks, int& e0, int& e1) {
@@ -59,18 +71,23 @@ __device__ __forceinline__ void rope_pieces(int c, int rot_chunks, int& e0, int&
   }
 }
 
-// cos and sin (times m, and the sine's sign) of chunk c's 8 pairs at position pos.
+// (cos, sin) of position times frequency, times m.
+__device__ __forceinline__ float2 rope_angle(double inv_freq, int pos, float mscale) {
+  const double turns = (double)pos * 0.15915494309189533576888 * inv_freq;  // 1 / (2 pi)
+  const float r = (float)(turns - rint(turns));
+  float s, co;
+  sincospif(2.f * r, &s, &co);
+  return make_float2(co * mscale, s * mscale);
+}
+
+// The same of chunk c's 8 pairs at position pos, the sine with a sign.
 __device__ __forceinline__ void rope_angles(const double* inv_freq, int c, int pos, float mscale,
                                             float sin_sign, float (&cs)[8], float (&sn)[8]) {
-  const double p = (double)pos * 0.15915494309189533576888;  // 1 / (2 pi): turns per radian
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const double turns = p * __ldg(inv_freq + 8 * c + i);
-    const float r = (float)(turns - rint(turns));
-    float s, co;
-    sincospif(2.f * r, &s, &co);
-    cs[i] = co * mscale;
-    sn[i] = s * (mscale * sin_sign);
+    const float2 a = rope_angle(__ldg(inv_freq + 8 * c + i), pos, mscale);
+    cs[i] = a.x;
+    sn[i] = a.y * sin_sign;
   }
 }
 
@@ -108,32 +125,48 @@ __global__ void __launch_bounds__(kRopeThreads) attn_rope_kernel(const RopeParam
   const long long b = token / p.S;
   const int s = (int)(token - b * p.S);
   const bool turns = c < p.rot_chunks;
+  int e0, e1;
+  rope_pieces<INTERLEAVED>(c, p.rot_chunks, e0, e1);
+  const int h_begin = blockIdx.y * p.heads_per_block;
+  const int h_end = min(h_begin + p.heads_per_block, p.H);
+  const uint16_t* q_src = p.q + b * p.qs[0] + s * p.qs[2];
+  const uint16_t* k_src = p.k + b * p.ks[0] + s * p.ks[2];
+  uint16_t* q_dst = p.q_out + b * p.qos[0] + s * p.qos[2];
+  uint16_t* k_dst = p.k_out + b * p.kos[0] + s * p.kos[2];
+  // A few heads' pieces are in flight together: the kernel is bound by its loads
+  // and stores.
+  uint4 x0[kRopeBatch], x1[kRopeBatch];
+  auto load = [&](int h) {
+#pragma unroll
+    for (int i = 0; i < kRopeBatch; ++i) {
+      if (h + i < h_end) {
+        const uint16_t* src =
+            h + i < p.Hq ? q_src + (h + i) * p.qs[1] : k_src + (h + i - p.Hq) * p.ks[1];
+        x0[i] = ld_once_v4(src + e0);
+        x1[i] = ld_once_v4(src + e1);
+      }
+    }
+  };
   float cs[8], sn[8];
   if (turns) {
     const int pos = p.positions == nullptr ? s : __ldg(p.positions + b * p.pos_stride + s);
     rope_angles(p.inv_freq, c, pos, p.mscale, p.sin_sign, cs, sn);
   }
-  int e0, e1;
-  rope_pieces<INTERLEAVED>(c, p.rot_chunks, e0, e1);
-  const int h_begin = blockIdx.y * p.heads_per_block;
-  const int h_end = min(h_begin + p.heads_per_block, p.H);
-  for (int h = h_begin; h < h_end; ++h) {
-    const bool is_q = h < p.Hq;
-    const int hh = is_q ? h : h - p.Hq;
-    const long long* si = is_q ? p.qs : p.ks;
-    const long long* so = is_q ? p.qos : p.kos;
-    const uint16_t* src = (is_q ? p.q : p.k) + b * si[0] + hh * si[1] + s * si[2];
-    uint16_t* dst = (is_q ? p.q_out : p.k_out) + b * so[0] + hh * so[1] + s * so[2];
-    const uint4 x0 = *reinterpret_cast<const uint4*>(src + e0);
-    const uint4 x1 = *reinterpret_cast<const uint4*>(src + e1);
-    if (turns) {
-      float y[16];
-      rope_turn<INTERLEAVED>(x0, x1, cs, sn, y);
-      *reinterpret_cast<uint4*>(dst + e0) = pack_bf16x8(y);
-      *reinterpret_cast<uint4*>(dst + e1) = pack_bf16x8(y + 8);
-    } else {
-      *reinterpret_cast<uint4*>(dst + e0) = x0;
-      *reinterpret_cast<uint4*>(dst + e1) = x1;
+  for (int h = h_begin; h < h_end; h += kRopeBatch) {
+    load(h);
+#pragma unroll
+    for (int i = 0; i < kRopeBatch; ++i) {
+      if (h + i < h_end) {
+        uint16_t* dst = h + i < p.Hq ? q_dst + (h + i) * p.qos[1] : k_dst + (h + i - p.Hq) * p.kos[1];
+        if (turns) {
+          float y[16];
+          rope_turn<INTERLEAVED>(x0[i], x1[i], cs, sn, y);
+          x0[i] = pack_bf16x8(y);
+          x1[i] = pack_bf16x8(y + 8);
+        }
+        *reinterpret_cast<uint4*>(dst + e0) = x0[i];
+        *reinterpret_cast<uint4*>(dst + e1) = x1[i];
+      }
     }
   }
 }
