@@ -545,6 +545,9 @@ __global__ void __launch_bounds__(384, 1)
       const int cmin = (int)(cm < 0 ? 0 : (cm > 64 ? 64 : cm));
       const int cmax = MASKS ? (int)(cx < 0 ? 0 : (cx > 64 ? 64 : cx)) : 64;
       const bool edge = __any_sync(0xffffffffu, cmin > 0 || cmax < 64);
+      // the columns this key is visible to, as two words of bits (masked kernels)
+      const uint32_t vis[2] = {low_bits(cmax) & ~low_bits(cmin),
+                               low_bits(cmax - 32) & ~low_bits(cmin - 32)};
       if (!(ok = mbar_wait_warp(bar(C::KB_SF), n & 1u, abort_flag))) break;
       tc_fence_after_sync();
       float pr[64];
@@ -577,10 +580,17 @@ __global__ void __launch_bounds__(384, 1)
           split_f32x2(fma_f32x2(f32x2(__uint_as_float(s2), __uint_as_float(s3)), c2x2,
                                 f32x2(nl.z, nl.w)), x2, x3);
           if (edge) {
-            x0 = bwd_keep(c >= cmin && c < cmax, x0);
-            x1 = bwd_keep(c + 1 >= cmin && c + 1 < cmax, x1);
-            x2 = bwd_keep(c + 2 >= cmin && c + 2 < cmax, x2);
-            x3 = bwd_keep(c + 3 >= cmin && c + 3 < cmax, x3);
+            if constexpr (MASKS) {
+              x0 = bwd_keep(vis[c >> 5] & (1u << (c & 31)), x0);
+              x1 = bwd_keep(vis[c >> 5] & (2u << (c & 31)), x1);
+              x2 = bwd_keep(vis[c >> 5] & (4u << (c & 31)), x2);
+              x3 = bwd_keep(vis[c >> 5] & (8u << (c & 31)), x3);
+            } else {
+              x0 = bwd_keep(c >= cmin, x0);
+              x1 = bwd_keep(c + 1 >= cmin, x1);
+              x2 = bwd_keep(c + 2 >= cmin, x2);
+              x3 = bwd_keep(c + 3 >= cmin, x3);
+            }
           }
           pr[c] = ex2(x0);
           pr[c + 1] = ex2(x1);
@@ -890,6 +900,10 @@ __global__ void __launch_bounds__(384, 1)
       const long long cs = MASKS ? (long long)p.sinks - t0 : 0;
       const int csink = MASKS ? (int)(cs < 0 ? 0 : (cs > 64 ? 64 : cs)) : 0;
       const bool edge = __any_sync(0xffffffffu, cmax < 64 || cmin > 0);
+      uint32_t vis[2];  // the visible columns as words of bits (masked kernels)
+#pragma unroll
+      for (int w = 0; w < 2; ++w)
+        vis[w] = low_bits(cmax - 32 * w) & (~low_bits(cmin - 32 * w) | low_bits(csink - 32 * w));
       if (!(ok = mbar_wait_warp(bar(C::QB_SF + (n & 1)), (n >> 1) & 1u, abort_flag))) break;
       tc_fence_after_sync();
       const uint32_t t_s = tmem + lane_off + ((n & 1) ? C::Q_TM_S1 : C::Q_TM_S0) + c0;
@@ -909,8 +923,8 @@ __global__ void __launch_bounds__(384, 1)
           split_f32x2(fma_f32x2(f32x2(__uint_as_float(s0), __uint_as_float(s1)), c2x2, nlx2), x0,
                       x1);
           if (edge) {
-            x0 = bwd_keep(c < cmax && (c >= cmin || (MASKS && c < csink)), x0);
-            x1 = bwd_keep(c + 1 < cmax && (c + 1 >= cmin || (MASKS && c + 1 < csink)), x1);
+            x0 = bwd_keep(MASKS ? (vis[c >> 5] & (1u << (c & 31))) != 0 : c < cmax, x0);
+            x1 = bwd_keep(MASKS ? (vis[c >> 5] & (2u << (c & 31))) != 0 : c + 1 < cmax, x1);
           }
           pr[c] = ex2(x0);
           pr[c + 1] = ex2(x1);
