@@ -20,6 +20,8 @@ from ._binding import (  # noqa: F401
     attn_fwd_block_sparse,
     attn_decode_paged,
     attn_decode_paged_fp8,
+    attn_decode_paged_window,
+    attn_decode_paged_window_fp8,
     attn_decode_workspace_size,
     attn_fwd,
     attn_fwd_fp8,

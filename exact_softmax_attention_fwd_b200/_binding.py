@@ -74,6 +74,8 @@ SIGNATURES = {
                                                                            _SZ, _P]),
     "attn_bwd_window_sinks_workspace_size": (_SZ, [_I] * 8),
     "attn_bwd_window_sinks": (_I, [_P] * 9 + [_I] * 6 + [_F, _P, _I, _I, _P, _SZ, _P]),
+    "attn_decode_paged_window": (_I, [_P] * 5 + [_I] * 7 + [_F, _I, _I, _P, _P, _P]),
+    "attn_decode_paged_window_fp8": (_I, [_P] * 7 + [_I] * 7 + [_F, _I, _I, _P, _P, _P]),
     "attn_rope": (_I, [_P] * 6 + [_LL] + [_I] * 7 + [_F, _P, _P]),
     "attn_rope_bwd": (_I, [_P] * 6 + [_LL] + [_I] * 7 + [_F, _P, _P]),
     "attn_append_paged": (_I, [_P] * 11 + [_I] * 4 + [_LL] + [_I] * 5 + [_F, _P, _P]),
@@ -1072,6 +1074,62 @@ def attn_fwd_paged_window(q, k_cache, v_cache, block_table, cu_seqlens_q, seq_le
             Hq, cache[2], total, max_seqlen_q, table[1], cache[0], d,
             float(scale), int(window), int(sinks), out.data_ptr(), _addr(lse), ws, ws_bytes, raw)
     return out, lse
+
+
+def _decode_window(name, q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, scale,
+                   window, sinks, out, lse, return_lse, stream):
+    import torch
+    bf16 = torch.bfloat16
+    fp8 = k_scale is not None
+    index = _device_index(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, out, lse)
+    raw = _raw_stream(stream, index)
+    qs, cache, table = q.shape, k_cache.shape, block_table.shape
+    if len(qs) != 3 or len(cache) != 4 or v_cache.shape != cache or cache[3] != qs[2]:
+        raise ValueError("q [B, Hq, d]; caches [num_pages, page_size, Hkv, d]")
+    B, Hq, d = qs
+    if q.dtype is not bf16 or not q.is_contiguous():
+        raise ValueError("q must be contiguous bfloat16")
+    dtype = torch.uint8 if fp8 else bf16
+    for t in (k_cache, v_cache):
+        if t.dtype is not dtype or not t.is_contiguous():
+            raise ValueError(f"the caches must be contiguous {dtype}")
+    scales = ()
+    if fp8:
+        for t in (k_scale, v_scale):
+            if t.dtype is not torch.float32 or t.shape != (cache[0], cache[2]) \
+                    or not t.is_contiguous():
+                raise ValueError("scales must be contiguous float32 [num_pages, Hkv]")
+        scales = (k_scale.data_ptr(), v_scale.data_ptr())
+    if len(table) != 2 or table[0] != B or block_table.dtype is not torch.int32 \
+            or not block_table.is_contiguous():
+        raise ValueError("block_table must be contiguous int32 [B, max_pages_per_seq]")
+    _int32(seq_lens, (B,), "seq_lens")
+    out = _buffer(out, q, qs, bf16, stream, "out")
+    if lse is not None or return_lse:
+        lse = _buffer(lse, q, (B, Hq), torch.float32, stream, "lse")
+    _launch(name, index, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), *scales,
+            block_table.data_ptr(), seq_lens.data_ptr(), cache[1], B, Hq, cache[2], d, table[1],
+            cache[0], float(scale), int(window), int(sinks), out.data_ptr(), _addr(lse), raw)
+    return out, lse
+
+
+def attn_decode_paged_window(q, k_cache, v_cache, block_table, seq_lens, scale: float, window: int,
+                             sinks: int = 0, out=None, lse=None, return_lse: bool = True,
+                             stream=None):
+    """Single-query attention over a paged cache with a sliding window (0: none) and the first
+    ``sinks`` tokens visible (layouts as attn_decode_paged; no workspace)."""
+    return _decode_window("attn_decode_paged_window", q, k_cache, v_cache, None, None, block_table,
+                          seq_lens, scale, window, sinks, out, lse, return_lse, stream)
+
+
+def attn_decode_paged_window_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
+                                 scale: float, window: int, sinks: int = 0, out=None, lse=None,
+                                 return_lse: bool = True, stream=None):
+    """attn_decode_paged_window over an E4M3 cache (layouts as attn_decode_paged_fp8)."""
+    if k_scale is None or v_scale is None:
+        raise ValueError("an E4M3 cache needs k_scale and v_scale")
+    return _decode_window("attn_decode_paged_window_fp8", q, k_cache, v_cache, k_scale, v_scale,
+                          block_table, seq_lens, scale, window, sinks, out, lse, return_lse, stream)
 
 
 def attn_get_device_error(stream=None):

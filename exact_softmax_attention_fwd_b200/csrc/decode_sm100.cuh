@@ -228,124 +228,53 @@ __device__ __forceinline__ void ldsm_m16n16_trans_b8(uint32_t (&r)[2], uint32_t 
                : "r"(addr));
 }
 
+// The state of one warp that attends the query heads of one KV head, 16 tokens
+// (a chunk) at a time: the MMA operand q, the online softmax of head row g, and
+// the accumulator O^T.  Used by the split kernel below and by the windowed
+// decode kernel, which differ in the chunks they walk and in what becomes of
+// the result.
 template <int D, bool FP8>
-__global__ void __launch_bounds__(32, 8) attn_decode_split_tma_kernel(
-    const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-    const DecodeFp8Params f) {
+struct DecodeWarp {
   using C = DecodeTmaCfg<D, FP8>;
-  constexpr int NH = C::NH;
-  constexpr int KW = D * C::E / 16;   // 32-bit words of a thread's K quarter row
-  const DecodeParams& p = f.d;
-  decode_allow_dependents();  // the merge grid may start filling in as CTAs retire
-  extern __shared__ uint8_t smem_raw[];
-  const uint32_t raw_addr = smem_u32(smem_raw);
-  const uint32_t sbase = (raw_addr + 1023u) & ~1023u;
-  const uint32_t bars = sbase + C::STAGES * C::STAGE;
-  const int lane = threadIdx.x;
-  const int kvh = (int)(blockIdx.x % (unsigned)p.Hkv);
-  const int split = (int)(blockIdx.x / (unsigned)p.Hkv);
-  const int b = blockIdx.z;
-  const int len = decode_clamped_len(p, b, lane == 0 && split == 0 && kvh == 0);
-  const int t_begin = split * kSplitTokens;
-  if (t_begin >= len) return;  // the merge kernel never reads splits past the end
-  const int t_end = min(t_begin + kSplitTokens, len);
-  const int n_chunks = (t_end - t_begin + 15) / 16;
-  const int n_steps = (n_chunks + NH - 1) / NH;
-  const int g = lane >> 2;   // MMA group id: head row of S / P, d-row block of V^T
-  const int tq = lane & 3;   // thread within the group
-  const int hq0 = kvh * p.group;
+  static constexpr int NH = C::NH;
+  static constexpr int KW = D * C::E / 16;  // 32-bit words of a thread's K quarter row
 
-  // q rows first: their loads need no page and overlap the block-table reads
-  uint32_t qraw[D / 8];
-  if (g < p.group) {
-    const uint16_t* src = p.q + ((size_t)b * p.Hq + hq0 + g) * D + (D / 4) * tq;
-#pragma unroll
-    for (int w = 0; w < D / 32; ++w) {
-      const uint4 x = *reinterpret_cast<const uint4*>(src + 8 * w);
-      qraw[4 * w + 0] = x.x;
-      qraw[4 * w + 1] = x.y;
-      qraw[4 * w + 2] = x.z;
-      qraw[4 * w + 3] = x.w;
-    }
-  } else {
-#pragma unroll
-    for (int w = 0; w < D / 8; ++w) qraw[w] = 0u;
-  }
+  int lane, g, tq;  // g: MMA group id (head row of S / P, d-row block of V^T); tq: thread in it
+  uint32_t qa[D / 16][2];  // q as the A operand (rows = heads, padded to 16)
+  float qscale;            // E4M3 caches: q was scaled by 1 / qscale into f16's range
+  float c2;
+  bool scale_pos;
+  float m_run;   // exponent base of head row g (log2 units)
+  float l_run;   // sum of P (f32): the LSE
+  float lr_run;  // sum of the weights the MMA applies: normalises O
+  float acc[D / 16][4];
 
-  // this lane's chunk: its page (or -1 when the id is outside the pool, or
-  // past the split) and scales
-  int my_page = -1;
-  float my_ks = 0.f, my_vs = 0.f;
-  if (lane < n_chunks) {
-    const int t = t_begin + 16 * lane;
-    const int pg = p.block_table[(size_t)b * p.max_pages + t / p.page_size];
-    if (pg >= 0 && pg < p.num_pages) {
-      my_page = pg;
-      if (FP8) {
-        my_ks = __ldg(f.k_scale + (size_t)pg * p.Hkv + kvh);
-        my_vs = __ldg(f.v_scale + (size_t)pg * p.Hkv + kvh);
+  // The raw bf16 words of this thread's quarter of query row `src` (head row g), issued
+  // early: their loads need no page and overlap the block-table reads.
+  __device__ __forceinline__ void load_q(uint32_t (&qraw)[D / 8], const uint16_t* q, size_t row,
+                                         int group) {
+    lane = threadIdx.x & 31;
+    g = lane >> 2;
+    tq = lane & 3;
+    if (g < group) {
+      const uint16_t* src = q + (row + g) * D + (D / 4) * tq;
+#pragma unroll
+      for (int w = 0; w < D / 32; ++w) {
+        const uint4 x = *reinterpret_cast<const uint4*>(src + 8 * w);
+        qraw[4 * w + 0] = x.x;
+        qraw[4 * w + 1] = x.y;
+        qraw[4 * w + 2] = x.z;
+        qraw[4 * w + 3] = x.w;
       }
     } else {
-      flag_device_error(kDevErrBadPage);
+#pragma unroll
+      for (int w = 0; w < D / 8; ++w) qraw[w] = 0u;
     }
   }
-  if (lane == 0) {
-    for (int s = 0; s < C::STAGES; ++s) mbar_init(bars + 8u * s, 1);
-    mbar_init_fence();
-    tma_prefetch_map(&tm_k);
-    tma_prefetch_map(&tm_v);
-  }
-  __syncwarp();
-  // Step i's copies into slot i % C::STAGES (lane 0; every lane takes part in
-  // the shuffles).  Chunks on a bad page, or past the split, add no bytes.
-  auto issue = [&](int i) {
-    int pg[NH];
-#pragma unroll
-    for (int h = 0; h < NH; ++h) pg[h] = __shfl_sync(0xffffffffu, my_page, NH * i + h);
-    if (lane == 0) {
-      const int slot = i % C::STAGES;
-      const uint32_t bar = bars + 8u * slot;
-      uint32_t bytes = 0;
-#pragma unroll
-      for (int h = 0; h < NH; ++h) bytes += pg[h] >= 0 ? (uint32_t)C::CHUNK : 0u;
-      fence_proxy_async_smem();  // the warp's reads of this slot precede the refill
-      mbar_arrive_expect_tx(bar, bytes);
-#pragma unroll
-      for (int h = 0; h < NH; ++h) {
-        if (pg[h] < 0) continue;
-        const uint32_t dst = sbase + slot * C::STAGE + h * C::CHUNK;
-        const int tok = pg[h] * p.page_size + (t_begin + 16 * (NH * i + h)) % p.page_size;
-#pragma unroll
-        for (int bx = 0; bx < C::NBOX; ++bx) {
-          const int col = bx * (C::BOX_BYTES / C::E);
-          tma_load_3d(dst + bx * 16 * C::BOX_BYTES, &tm_k, bar, col, kvh, tok);
-          tma_load_3d(dst + C::TILE + bx * 16 * C::BOX_BYTES, &tm_v, bar, col, kvh, tok);
-        }
-      }
-    }
-  };
-  int n_issued = 0;
-  for (; n_issued < C::STAGES && n_issued < n_steps; ++n_issued) issue(n_issued);
-  // E4M3: the largest V scale magnitude of the split's pages (bad pages hold 0)
-  float vmax = FP8 ? fabsf(my_vs) : 1.f;
-  if (FP8) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, o));
-    if (!(vmax > 0.f)) vmax = 1.f;
-  }
-  const float inv_vmax = FP8 ? 1.f / vmax : 1.f;
-  // E4M3: this lane's chunk's factor on P (|.| <= 1) and the factor that takes
-  // the applied weights back to weights on the dequantised V (0 marks a zero
-  // scale, whose weights count as f16(P))
-  const float my_rv = my_vs * inv_vmax;
-  const float my_back = (FP8 && my_vs != 0.f) ? vmax / my_vs : 0.f;
 
-  // q as the A operand (rows = heads, padded to 16; layout as the register
-  // kernels).  E4M3 caches: f16 q scaled by 2^-qe into f16's range.
-  uint32_t qa[D / 16][2];
-  float qscale = 1.f;
-  {
-    const uint32_t (&raw)[D / 8] = qraw;
+  // q into MMA form (E4M3 caches: f16 q scaled by 2^-qe into f16's range), empty sums.
+  __device__ __forceinline__ void begin(const uint32_t (&raw)[D / 8], float scale_log2) {
+    qscale = 1.f;
     if (!FP8) {
 #pragma unroll
       for (int w = 0; w < D / 8; ++w) qa[w >> 1][w & 1] = raw[w];
@@ -366,38 +295,23 @@ __global__ void __launch_bounds__(32, 8) attn_decode_split_tma_kernel(
         qa[w >> 1][w & 1] = pack_f16x2(__uint_as_float(raw[w] << 16) * qinv,
                                        __uint_as_float(raw[w] & 0xFFFF0000u) * qinv);
     }
+    c2 = scale_log2;
+    scale_pos = c2 > 0.f;
+    if (!scale_pos) c2 = 1.f;
+    m_run = -INFINITY;
+    l_run = lr_run = 0.f;
+#pragma unroll
+    for (int mc = 0; mc < D / 16; ++mc) acc[mc][0] = acc[mc][1] = acc[mc][2] = acc[mc][3] = 0.f;
   }
 
-  const float my_kq = my_ks * qscale;  // E4M3: K scale times the power of two on q
-  float c2 = p.scale_log2;
-  const bool scale_pos = c2 > 0.f;
-  if (!scale_pos) c2 = 1.f;
-  float m_run = -INFINITY;  // exponent base of head row g (log2 units)
-  float l_run = 0.f;        // sum of P (f32): the LSE
-  float lr_run = 0.f;       // sum of the weights the MMA applies: normalises O
-  float acc[D / 16][4];
-#pragma unroll
-  for (int mc = 0; mc < D / 16; ++mc) acc[mc][0] = acc[mc][1] = acc[mc][2] = acc[mc][3] = 0.f;
-
-  int i = 0;
-#pragma unroll 1
-  for (; i < n_steps; ++i) {
-    const int slot = i % C::STAGES;
-    int n_here[NH];
-    float kqc[NH], rvc[NH], backc[NH];
-#pragma unroll
-    for (int h = 0; h < NH; ++h) {
-      const int c = NH * i + h;
-      const int pg = __shfl_sync(0xffffffffu, my_page, c);
-      n_here[h] = pg >= 0 ? min(16, t_end - (t_begin + 16 * c)) : 0;  // <= 0 past the end
-      kqc[h] = FP8 ? __shfl_sync(0xffffffffu, my_kq, c) : 1.f;
-      rvc[h] = FP8 ? __shfl_sync(0xffffffffu, my_rv, c) : 1.f;
-      backc[h] = FP8 ? __shfl_sync(0xffffffffu, my_back, c) : 1.f;
-    }
-    const uint32_t st = sbase + slot * C::STAGE;
-    const bool landed = mbar_wait(bars + 8u * slot, (uint32_t)(i / C::STAGES) & 1u, nullptr);
-    if (!__all_sync(0xffffffffu, landed)) break;  // timed out: flagged, wind down
-
+  // One step: NH chunks whose K and V rows lie in the ring slot at `st`.
+  // vis[h]: bit i is set iff token i of chunk h counts (others may hold
+  // anything).  E4M3 caches: kqc, rvc, backc as described at the split kernel.
+  // `read_done` runs as soon as the warp has read the slot.
+  template <typename ReadDone>
+  __device__ __forceinline__ void step(uint32_t st, float scale_log2, const uint32_t (&vis)[NH],
+                                       const float (&kqc)[NH], const float (&rvc)[NH],
+                                       const float (&backc)[NH], ReadDone read_done) {
     // ---- S = q K^T (16 padded head rows x 16 tokens per chunk); two
     // independent accumulation chains (even and odd d-chunks), summed
     float s4[NH][4];
@@ -445,14 +359,14 @@ __global__ void __launch_bounds__(32, 8) attn_decode_split_tma_kernel(
     for (int h = 0; h < NH; ++h) {
       if (!scale_pos) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s4[h][e] *= p.scale_log2;
+        for (int e = 0; e < 4; ++e) s4[h][e] *= scale_log2;
       }
-      // tokens past the length or on a bad page: their K rows may hold anything
-      // (only their own score columns see them), masked here
-      if (n_here[h] < 16) {
+      // tokens that do not count: their K rows may hold anything (only their
+      // own score columns see them), masked here
+      if (vis[h] != 0xFFFFu) {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          if ((FP8 ? 4 * tq + e : (e >> 1) * 8 + 2 * tq + (e & 1)) >= n_here[h])
+          if (!((vis[h] >> (FP8 ? 4 * tq + e : (e >> 1) * 8 + 2 * tq + (e & 1))) & 1u))
             s4[h][e] = -INFINITY;
       }
       mx = fmaxf(mx, fmaxf(fmaxf(s4[h][0], s4[h][1]), fmaxf(s4[h][2], s4[h][3])));
@@ -527,20 +441,21 @@ __global__ void __launch_bounds__(32, 8) attn_decode_split_tma_kernel(
           vw[h][mc][3] = r[3];
         }
       }
-      if (n_here[h] < 16) {  // masked tokens must not inject NaN
+      if (vis[h] != 0xFFFFu) {  // masked tokens must not inject NaN
         if constexpr (FP8) {
-          const int keep = min(max(n_here[h] - 4 * tq, 0), 4);  // bytes = tokens 4tq + b
-          const uint32_t m = keep >= 4 ? 0xFFFFFFFFu : ((1u << (8 * keep)) - 1u);
+          const uint32_t four = vis[h] >> (4 * tq);  // bytes = tokens 4tq + b
+          const uint32_t m = ((four & 1u) ? 0xFFu : 0u) | ((four & 2u) ? 0xFF00u : 0u) |
+                             ((four & 4u) ? 0xFF0000u : 0u) | ((four & 8u) ? 0xFF000000u : 0u);
 #pragma unroll
           for (int mc = 0; mc < D / 16; ++mc) {
             vw[h][mc][0] &= m;
             vw[h][mc][1] &= m;
           }
         } else {
-          const int t0 = 2 * tq;
-          const uint32_t m_lo = (t0 < n_here[h] ? 0xFFFFu : 0u) | (t0 + 1 < n_here[h] ? 0xFFFF0000u : 0u);
+          const uint32_t two = vis[h] >> (2 * tq);
+          const uint32_t m_lo = ((two & 1u) ? 0xFFFFu : 0u) | ((two & 2u) ? 0xFFFF0000u : 0u);
           const uint32_t m_hi =
-              (t0 + 8 < n_here[h] ? 0xFFFFu : 0u) | (t0 + 9 < n_here[h] ? 0xFFFF0000u : 0u);
+              ((two & 0x100u) ? 0xFFFFu : 0u) | ((two & 0x200u) ? 0xFFFF0000u : 0u);
 #pragma unroll
           for (int mc = 0; mc < D / 16; ++mc) {
             vw[h][mc][0] &= m_lo;
@@ -551,8 +466,8 @@ __global__ void __launch_bounds__(32, 8) attn_decode_split_tma_kernel(
         }
       }
     }
-    __syncwarp();  // every lane has read the slot: refill it with step i + C::STAGES
-    if (n_issued < n_steps) issue(n_issued++);
+    __syncwarp();  // every lane has read the slot
+    read_done();
     if (__any_sync(0xffffffffu, alpha != 1.f)) {  // some head row moved its base
       const float a_h0 = __shfl_sync(0xffffffffu, alpha, (2 * tq) * 4);
       const float a_h1 = __shfl_sync(0xffffffffu, alpha, (2 * tq + 1) * 4);
@@ -580,6 +495,148 @@ __global__ void __launch_bounds__(32, 8) attn_decode_split_tma_kernel(
       }
     }
   }
+
+  // The row sums were kept per lane: every lane of a head row shares its base.
+  __device__ __forceinline__ void finish_sums() {
+    l_run += __shfl_xor_sync(0xffffffffu, l_run, 1);
+    lr_run += __shfl_xor_sync(0xffffffffu, lr_run, 1);
+    l_run += __shfl_xor_sync(0xffffffffu, l_run, 2);
+    lr_run += __shfl_xor_sync(0xffffffffu, lr_run, 2);
+  }
+};
+
+// The copies of one step's chunks into a ring slot, issued by lane 0: chunk h
+// from pool token tok[h] (skipped, adding no bytes, when it is negative).
+template <int D, bool FP8>
+__device__ __forceinline__ void decode_issue(const CUtensorMap* tm_k, const CUtensorMap* tm_v,
+                                             uint32_t dst0, uint32_t bar, int kvh,
+                                             const int (&tok)[DecodeTmaCfg<D, FP8>::NH]) {
+  using C = DecodeTmaCfg<D, FP8>;
+  uint32_t bytes = 0;
+#pragma unroll
+  for (int h = 0; h < C::NH; ++h) bytes += tok[h] >= 0 ? (uint32_t)C::CHUNK : 0u;
+  fence_proxy_async_smem();  // the warp's reads of this slot precede the refill
+  mbar_arrive_expect_tx(bar, bytes);
+#pragma unroll
+  for (int h = 0; h < C::NH; ++h) {
+    if (tok[h] < 0) continue;
+    const uint32_t dst = dst0 + h * C::CHUNK;
+#pragma unroll
+    for (int bx = 0; bx < C::NBOX; ++bx) {
+      const int col = bx * (C::BOX_BYTES / C::E);
+      tma_load_3d(dst + bx * 16 * C::BOX_BYTES, tm_k, bar, col, kvh, tok[h]);
+      tma_load_3d(dst + C::TILE + bx * 16 * C::BOX_BYTES, tm_v, bar, col, kvh, tok[h]);
+    }
+  }
+}
+
+template <int D, bool FP8>
+__global__ void __launch_bounds__(32, 8) attn_decode_split_tma_kernel(
+    const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+    const DecodeFp8Params f) {
+  using C = DecodeTmaCfg<D, FP8>;
+  constexpr int NH = C::NH;
+  const DecodeParams& p = f.d;
+  decode_allow_dependents();  // the merge grid may start filling in as CTAs retire
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_addr = smem_u32(smem_raw);
+  const uint32_t sbase = (raw_addr + 1023u) & ~1023u;
+  const uint32_t bars = sbase + C::STAGES * C::STAGE;
+  const int lane = threadIdx.x;
+  const int kvh = (int)(blockIdx.x % (unsigned)p.Hkv);
+  const int split = (int)(blockIdx.x / (unsigned)p.Hkv);
+  const int b = blockIdx.z;
+  const int len = decode_clamped_len(p, b, lane == 0 && split == 0 && kvh == 0);
+  const int t_begin = split * kSplitTokens;
+  if (t_begin >= len) return;  // the merge kernel never reads splits past the end
+  const int t_end = min(t_begin + kSplitTokens, len);
+  const int n_chunks = (t_end - t_begin + 15) / 16;
+  const int n_steps = (n_chunks + NH - 1) / NH;
+  const int hq0 = kvh * p.group;
+
+  DecodeWarp<D, FP8> w;
+  uint32_t qraw[D / 8];
+  w.load_q(qraw, p.q, (size_t)b * p.Hq + hq0, p.group);
+
+  // this lane's chunk: its page (or -1 when the id is outside the pool, or
+  // past the split), which of its tokens count, and its scales
+  int my_page = -1;
+  uint32_t my_vis = 0;
+  float my_ks = 0.f, my_vs = 0.f;
+  if (lane < n_chunks) {
+    const int t = t_begin + 16 * lane;
+    const int pg = p.block_table[(size_t)b * p.max_pages + t / p.page_size];
+    if (pg >= 0 && pg < p.num_pages) {
+      my_page = pg;
+      my_vis = t_end - t >= 16 ? 0xFFFFu : (1u << (t_end - t)) - 1u;
+      if (FP8) {
+        my_ks = __ldg(f.k_scale + (size_t)pg * p.Hkv + kvh);
+        my_vs = __ldg(f.v_scale + (size_t)pg * p.Hkv + kvh);
+      }
+    } else {
+      flag_device_error(kDevErrBadPage);
+    }
+  }
+  if (lane == 0) {
+    for (int s = 0; s < C::STAGES; ++s) mbar_init(bars + 8u * s, 1);
+    mbar_init_fence();
+    tma_prefetch_map(&tm_k);
+    tma_prefetch_map(&tm_v);
+  }
+  __syncwarp();
+  // Step i's copies into slot i % C::STAGES (lane 0; every lane takes part in
+  // the shuffles).  Chunks on a bad page, or past the split, add no bytes.
+  auto issue = [&](int i) {
+    int tok[NH];
+#pragma unroll
+    for (int h = 0; h < NH; ++h) {
+      const int pg = __shfl_sync(0xffffffffu, my_page, NH * i + h);
+      tok[h] = pg < 0 ? -1 : pg * p.page_size + (t_begin + 16 * (NH * i + h)) % p.page_size;
+    }
+    if (lane == 0) {
+      const int slot = i % C::STAGES;
+      decode_issue<D, FP8>(&tm_k, &tm_v, sbase + slot * C::STAGE, bars + 8u * slot, kvh, tok);
+    }
+  };
+  int n_issued = 0;
+  for (; n_issued < C::STAGES && n_issued < n_steps; ++n_issued) issue(n_issued);
+  // E4M3: the largest V scale magnitude of the split's pages (bad pages hold 0)
+  float vmax = FP8 ? fabsf(my_vs) : 1.f;
+  if (FP8) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, o));
+    if (!(vmax > 0.f)) vmax = 1.f;
+  }
+  const float inv_vmax = FP8 ? 1.f / vmax : 1.f;
+  // E4M3: this lane's chunk's factor on P (|.| <= 1) and the factor that takes
+  // the applied weights back to weights on the dequantised V (0 marks a zero
+  // scale, whose weights count as f16(P))
+  const float my_rv = my_vs * inv_vmax;
+  const float my_back = (FP8 && my_vs != 0.f) ? vmax / my_vs : 0.f;
+
+  w.begin(qraw, p.scale_log2);
+  const float my_kq = my_ks * w.qscale;  // E4M3: K scale times the power of two on q
+
+  int i = 0;
+#pragma unroll 1
+  for (; i < n_steps; ++i) {
+    const int slot = i % C::STAGES;
+    uint32_t vis[NH];
+    float kqc[NH], rvc[NH], backc[NH];
+#pragma unroll
+    for (int h = 0; h < NH; ++h) {
+      const int c = NH * i + h;
+      vis[h] = __shfl_sync(0xffffffffu, my_vis, c);
+      kqc[h] = FP8 ? __shfl_sync(0xffffffffu, my_kq, c) : 1.f;
+      rvc[h] = FP8 ? __shfl_sync(0xffffffffu, my_rv, c) : 1.f;
+      backc[h] = FP8 ? __shfl_sync(0xffffffffu, my_back, c) : 1.f;
+    }
+    const bool landed = mbar_wait(bars + 8u * slot, (uint32_t)(i / C::STAGES) & 1u, nullptr);
+    if (!__all_sync(0xffffffffu, landed)) break;  // timed out: flagged, wind down
+    w.step(sbase + slot * C::STAGE, p.scale_log2, vis, kqc, rvc, backc, [&] {
+      if (n_issued < n_steps) issue(n_issued++);  // refill the slot with step i + C::STAGES
+    });
+  }
   // after a timed-out wait: no copy may still be landing when the CTA exits
   // (steps [i, n_issued) were issued but not consumed; bounded waits)
   if (lane == 0)
@@ -587,15 +644,11 @@ __global__ void __launch_bounds__(32, 8) attn_decode_split_tma_kernel(
       mbar_wait(bars + 8u * (j % C::STAGES), (uint32_t)(j / C::STAGES) & 1u, nullptr);
   __syncwarp();
 
-  // ---- this split's normalised partial output and its log2-sum-exp (the
-  // row sums were kept per lane: every lane of a head row shares its base)
-  l_run += __shfl_xor_sync(0xffffffffu, l_run, 1);
-  lr_run += __shfl_xor_sync(0xffffffffu, lr_run, 1);
-  l_run += __shfl_xor_sync(0xffffffffu, l_run, 2);
-  lr_run += __shfl_xor_sync(0xffffffffu, lr_run, 2);
-  const int h0 = 2 * tq, h1 = 2 * tq + 1;
-  const float l_h0 = __shfl_sync(0xffffffffu, lr_run, h0 * 4);
-  const float l_h1 = __shfl_sync(0xffffffffu, lr_run, h1 * 4);
+  // ---- this split's normalised partial output and its log2-sum-exp
+  w.finish_sums();
+  const int h0 = 2 * w.tq, h1 = 2 * w.tq + 1;
+  const float l_h0 = __shfl_sync(0xffffffffu, w.lr_run, h0 * 4);
+  const float l_h1 = __shfl_sync(0xffffffffu, w.lr_run, h1 * 4);
   const float inv0 = l_h0 > 0.f ? vmax / l_h0 : 0.f;  // vmax = 1 for a bf16 cache
   const float inv1 = l_h1 > 0.f ? vmax / l_h1 : 0.f;
 #pragma unroll
@@ -603,16 +656,16 @@ __global__ void __launch_bounds__(32, 8) attn_decode_split_tma_kernel(
     const int h = hh ? h1 : h0;
     if (h >= p.group) continue;
     const float inv = hh ? inv1 : inv0;
-    float* dst = p.o_part + (((size_t)b * p.Hq + hq0 + h) * p.n_split + split) * D + g;
+    float* dst = p.o_part + (((size_t)b * p.Hq + hq0 + h) * p.n_split + split) * D + w.g;
 #pragma unroll
     for (int mc = 0; mc < D / 16; ++mc) {
-      dst[16 * mc] = acc[mc][hh] * inv;
-      dst[16 * mc + 8] = acc[mc][2 + hh] * inv;
+      dst[16 * mc] = w.acc[mc][hh] * inv;
+      dst[16 * mc + 8] = w.acc[mc][2 + hh] * inv;
     }
   }
-  if (tq == 0 && g < p.group) {
-    const float lse2 = l_run > 0.f ? m_run + lg2(l_run) : -INFINITY;
-    p.lse_part[((size_t)b * p.Hq + hq0 + g) * p.n_split + split] = lse2;
+  if (w.tq == 0 && w.g < p.group) {
+    const float lse2 = w.l_run > 0.f ? w.m_run + lg2(w.l_run) : -INFINITY;
+    p.lse_part[((size_t)b * p.Hq + hq0 + w.g) * p.n_split + split] = lse2;
   }
 }
 

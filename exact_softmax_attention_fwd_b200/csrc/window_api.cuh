@@ -1,11 +1,135 @@
 // window_api.cuh -- the C entry points of attention with a sliding window and
 // visible first tokens (declared in attn.h): argument checks on the host, before
 // any CUDA call, and the launches.  Included by attn_api.cu, whose helpers it
-// uses; the kernels are the masked instantiations of the prefill and backward
-// kernels.
+// uses; prefill and backward are the masked instantiations of their kernels,
+// decode has a kernel of its own.
 #pragma once
 
+#include "decode_window_sm100.cuh"
+
+namespace attn_b200 {
+namespace {
+
+template <int D, bool FP8>
+int launch_decode_window(const CUtensorMap& mk, const CUtensorMap& mv, DecodeWindowParams& p,
+                         int max_chunks, cudaStream_t stream) {
+  using W = DecodeWinCfg<D, FP8>;
+  auto kern = attn_decode_window_kernel<D, FP8>;
+  static std::atomic<unsigned long long> smem_set{0};
+  if (!set_smem_once(kern, W::SMEM, smem_set)) return ATTN_ERR_CUDA;
+  const int sms = sm_count();
+  if (sms <= 0) return ATTN_ERR_CUDA;
+  // CTAs per (sequence, KV head): doubled while the grid leaves room for more
+  // (two CTAs an SM) and every warp keeps a step of its own
+  const long long pairs = (long long)p.f.d.B * p.f.d.Hkv;
+  int cs = 1;
+  while (cs < 8 && pairs * cs < 2ll * sms && 2 * cs * kWinWarps * DecodeTmaCfg<D, FP8>::NH <= max_chunks)
+    cs *= 2;
+  p.cluster = cs;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(pairs * cs));
+  cfg.blockDim = dim3(kWinWarps * 32);
+  cfg.dynamicSmemBytes = W::SMEM;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)cs;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kern, mk, mv, p) != cudaSuccess) return ATTN_ERR_CUDA;
+  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+int decode_window_run(bool fp8, const void* q, const void* k_cache, const void* v_cache,
+                      const float* k_scale, const float* v_scale, const int32_t* block_table,
+                      const int32_t* seq_lens, int page_size, int B, int Hq, int Hkv, int d,
+                      int max_pages_per_seq, int num_pages, float scale, int window, int sinks,
+                      void* o, float* lse, attn_stream_t stream) {
+  if (q == nullptr || k_cache == nullptr || v_cache == nullptr || block_table == nullptr ||
+      seq_lens == nullptr || o == nullptr)
+    return ATTN_ERR_INVALID_ARG;
+  if (fp8 && (k_scale == nullptr || v_scale == nullptr)) return ATTN_ERR_INVALID_ARG;
+  if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || max_pages_per_seq < 1 || num_pages < 1 ||
+      page_size < 1)
+    return ATTN_ERR_INVALID_ARG;
+  if ((long long)B * Hkv > (1ll << 27) || (long long)max_pages_per_seq * page_size > (1ll << 30) ||
+      (long long)num_pages * page_size > 0x7fffffffLL)
+    return ATTN_ERR_INVALID_ARG;
+  if (window < 0 || sinks < 0 || !std::isfinite(scale)) return ATTN_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
+  if (page_size % 16 != 0 || page_size > 256) return ATTN_ERR_UNSUPPORTED;
+  if (Hq / Hkv > 8) return ATTN_ERR_UNSUPPORTED;
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(o) ||
+      !aligned4(block_table) || !aligned4(seq_lens) || (lse != nullptr && !aligned4(lse)))
+    return ATTN_ERR_ALIGNMENT;
+  if (fp8 && (!aligned4(k_scale) || !aligned4(v_scale))) return ATTN_ERR_ALIGNMENT;
+  DecodeWindowParams p;
+  std::memset(&p, 0, sizeof(p));
+  DecodeParams& prm = p.f.d;
+  prm.q = static_cast<const uint16_t*>(q);
+  prm.block_table = block_table;
+  prm.seq_lens = seq_lens;
+  prm.o = static_cast<uint16_t*>(o);
+  prm.lse = lse;
+  prm.B = B;
+  prm.Hq = Hq;
+  prm.Hkv = Hkv;
+  prm.group = Hq / Hkv;
+  prm.page_size = page_size;
+  prm.max_pages = max_pages_per_seq;
+  prm.num_pages = num_pages;
+  prm.scale_log2 = scale * 1.4426950408889634f;
+  p.f.k_scale = k_scale;
+  p.f.v_scale = v_scale;
+  p.window = window > 0 ? window : INT_MAX;
+  p.sinks = window > 0 ? sinks : 0;
+  // the most chunks a sequence can have visible
+  const long long cap = (long long)max_pages_per_seq * page_size / 16;
+  const int max_chunks =
+      (int)std::min(cap, ((long long)p.window + 15) / 16 + 1 + ((long long)p.sinks + 15) / 16);
+  CUtensorMap mk, mv;
+  const long long pool_tokens = (long long)num_pages * page_size;
+  const bool maps_ok =
+      fp8 ? make_token_map_u8(&mk, k_cache, d, Hkv, pool_tokens) &&
+                make_token_map_u8(&mv, v_cache, d, Hkv, pool_tokens)
+          : make_token_map(&mk, k_cache, d, Hkv, pool_tokens, 16) &&
+                make_token_map(&mv, v_cache, d, Hkv, pool_tokens, 16);
+  if (!maps_ok) return ATTN_ERR_CUDA;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (d == 128)
+    return fp8 ? launch_decode_window<128, true>(mk, mv, p, max_chunks, st)
+               : launch_decode_window<128, false>(mk, mv, p, max_chunks, st);
+  return fp8 ? launch_decode_window<64, true>(mk, mv, p, max_chunks, st)
+             : launch_decode_window<64, false>(mk, mv, p, max_chunks, st);
+}
+
+}  // namespace
+}  // namespace attn_b200
+
 extern "C" {
+
+int attn_decode_paged_window(const void* q, const void* k_cache, const void* v_cache,
+                             const int32_t* block_table, const int32_t* seq_lens, int page_size,
+                             int B, int Hq, int Hkv, int d, int max_pages_per_seq, int num_pages,
+                             float scale, int window, int sinks, void* o, float* lse,
+                             attn_stream_t stream) {
+  return decode_window_run(false, q, k_cache, v_cache, nullptr, nullptr, block_table, seq_lens,
+                           page_size, B, Hq, Hkv, d, max_pages_per_seq, num_pages, scale, window,
+                           sinks, o, lse, stream);
+}
+
+int attn_decode_paged_window_fp8(const void* q, const void* k_cache, const void* v_cache,
+                                 const float* k_scale, const float* v_scale,
+                                 const int32_t* block_table, const int32_t* seq_lens,
+                                 int page_size, int B, int Hq, int Hkv, int d,
+                                 int max_pages_per_seq, int num_pages, float scale, int window,
+                                 int sinks, void* o, float* lse, attn_stream_t stream) {
+  return decode_window_run(true, q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
+                           page_size, B, Hq, Hkv, d, max_pages_per_seq, num_pages, scale, window,
+                           sinks, o, lse, stream);
+}
 
 int attn_fwd_window_sinks(const void* q, const void* k, const void* v, void* o, float* lse, int B,
                           int Hq, int Hkv, int Sq, int Sk, int d, float scale,

@@ -721,6 +721,39 @@ int attn_bwd_window_sinks(const void* q, const void* k, const void* v, const voi
                           const int32_t* k_lens, int window, int sinks, void* workspace,
                           size_t workspace_bytes, attn_stream_t stream);
 
+/*
+ * attn_decode_paged_window -- attn_decode_paged with a sliding window and
+ * visible first tokens: the query of a sequence of n keys sees keys j with
+ * j >= n - window or j < sinks (window = 0: every key).  Pages that hold none
+ * of them are not read, nor are their block-table entries; slots that are not
+ * visible may hold anything.
+ *   seq_lens 0 is allowed (O = 0, LSE = -inf).  No workspace: one kernel, a
+ *   cluster of 1 to 8 CTAs per (sequence, KV head), which merges its warps'
+ *   parts in shared memory in a fixed order.
+ *   page_size a positive multiple of 16 (<= 256); d in {64, 128};
+ *   Hq / Hkv <= 8; B * Hkv <= 2^27.
+ * Other arguments, layouts, device-side checks and errors as
+ * attn_decode_paged (INVALID_ARG also for a negative window or sinks).
+ */
+int attn_decode_paged_window(const void* q, const void* k_cache, const void* v_cache,
+                             const int32_t* block_table, const int32_t* seq_lens, int page_size,
+                             int B, int Hq, int Hkv, int d, int max_pages_per_seq, int num_pages,
+                             float scale, int window, int sinks, void* o, float* lse,
+                             attn_stream_t stream);
+
+/*
+ * attn_decode_paged_window_fp8 -- attn_decode_paged_window over the E4M3 cache
+ * of attn_decode_paged_fp8 (uint8 codes, one float32 scale per page and KV
+ * head), with the same arithmetic.  INVALID_ARG also for a NULL scale array,
+ * ALIGNMENT when one is not 4-byte aligned.
+ */
+int attn_decode_paged_window_fp8(const void* q, const void* k_cache, const void* v_cache,
+                                 const float* k_scale, const float* v_scale,
+                                 const int32_t* block_table, const int32_t* seq_lens,
+                                 int page_size, int B, int Hq, int Hkv, int d,
+                                 int max_pages_per_seq, int num_pages, float scale, int window,
+                                 int sinks, void* o, float* lse, attn_stream_t stream);
+
 /* attn_strerror -- static description of an attn_status value. */
 const char* attn_strerror(int status);
 

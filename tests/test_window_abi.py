@@ -87,3 +87,30 @@ def test_paged_validation(lib, kw, status):
 
 def test_paged_without_tokens_launches_nothing(lib):
     assert _paged(lib, total=0) == B.ATTN_OK
+
+
+def _decode(lib, fp8=False, q=FAKE, kc=FAKE, ks=FAKE, vs=FAKE, tbl=FAKE, lens=FAKE, page=16, B_=2,
+            Hq=4, Hkv=2, d=128, maxp=8, npages=20, scale=0.1, window=16, sinks=4, o=FAKE, lse=None):
+    fn = lib.attn_decode_paged_window_fp8 if fp8 else lib.attn_decode_paged_window
+    return fn(q, kc, FAKE, *((ks, vs) if fp8 else ()), tbl, lens, page, B_, Hq, Hkv, d, maxp, npages,
+              scale, window, sinks, o, lse, None)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("kw,status", [
+    (dict(q=None), B.ATTN_ERR_INVALID_ARG), (dict(tbl=None), B.ATTN_ERR_INVALID_ARG),
+    (dict(o=None), B.ATTN_ERR_INVALID_ARG), (dict(B_=0), B.ATTN_ERR_INVALID_ARG),
+    (dict(Hq=5), B.ATTN_ERR_INVALID_ARG), (dict(window=-1), B.ATTN_ERR_INVALID_ARG),
+    (dict(sinks=-1), B.ATTN_ERR_INVALID_ARG), (dict(scale=float("nan")), B.ATTN_ERR_INVALID_ARG),
+    (dict(maxp=1 << 27), B.ATTN_ERR_INVALID_ARG), (dict(npages=1 << 28), B.ATTN_ERR_INVALID_ARG),
+    (dict(page=8), B.ATTN_ERR_UNSUPPORTED), (dict(page=272), B.ATTN_ERR_UNSUPPORTED),
+    (dict(d=96), B.ATTN_ERR_UNSUPPORTED), (dict(Hq=18), B.ATTN_ERR_UNSUPPORTED),
+    (dict(kc=FAKE + 8), B.ATTN_ERR_ALIGNMENT), (dict(lens=FAKE + 1), B.ATTN_ERR_ALIGNMENT),
+    (dict(lse=FAKE + 2), B.ATTN_ERR_ALIGNMENT)])
+def test_decode_validation(lib, fp8, kw, status):
+    assert _decode(lib, fp8, **kw) == status
+
+
+def test_decode_fp8_scales(lib):
+    assert _decode(lib, True, vs=None) == B.ATTN_ERR_INVALID_ARG
+    assert _decode(lib, True, ks=FAKE + 2) == B.ATTN_ERR_ALIGNMENT
