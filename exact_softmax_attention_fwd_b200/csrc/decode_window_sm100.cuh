@@ -8,9 +8,9 @@
 //
 // What bounds it: the visible keys' bytes, or, for few sequences, the latency of
 // one pass.  A window bounds the keys of a sequence whatever its length, so that
-// they fit one cluster of CTAs at most: a cluster of 1 to 8 CTAs of 4 warps takes
-// one (sequence, KV head), each warp an equal run of its 16-token chunks, and
-// the warps' partial results (running maximum, sums and accumulator) are
+// they fit one cluster of CTAs at most: a CTA of 1 to 4 warps, or a cluster of 2
+// to 8 CTAs of 4 warps, takes one (sequence, KV head) (which of these: see
+// win_shape), each warp an equal run of its 16-token chunks, and the warps' partial results (running maximum, sums and accumulator) are
 // merged in shared memory, first within each CTA, then across the cluster's
 // CTAs through distributed shared memory.  So there is one launch, no
 // workspace, and no partial result in memory; the merge's order is fixed, so
@@ -26,7 +26,7 @@
 
 namespace attn_b200 {
 
-constexpr int kWinWarps = 4;  // per CTA
+constexpr int kWinWarps = 4;  // per CTA, at most
 
 struct DecodeWindowParams {
   DecodeFp8Params f;   // o_part, lse_part, n_split unused
@@ -38,14 +38,54 @@ template <int D, bool FP8>
 struct DecodeWinCfg {
   using C = DecodeTmaCfg<D, FP8>;
   static constexpr int RING = C::STAGES * C::STAGE;  // of one warp
-  static constexpr int OFF_BARS = kWinWarps * RING;
-  static constexpr int OFF_PART = OFF_BARS + kWinWarps * C::STAGES * 8;  // this CTA's merged part
-  // merged part: O [8][D] (sums of weights times values), then m, l, lr [8] each
+  static constexpr int BARS = 128;                   // all warps' mbarriers
+  // a merged part: O [8][D] (sums of weights times values), then m, l, lr [8] each
   static constexpr int PART = 8 * D * 4 + 3 * 8 * 4;
-  static constexpr int OFF_PART_A = (OFF_PART + 15) / 16 * 16;
-  static constexpr int SMEM = OFF_PART_A + PART + 1024;  // + runtime 1024-byte alignment
+  // a CTA of n warps: their rings, barriers, its part; + runtime 1024-byte alignment
+  __host__ __device__ static constexpr int smem(int n) { return n * RING + BARS + PART + 1024; }
+  // CTAs of n warps that fit an SM: 227 KB, and 64 K registers at MAX_REGS a thread
+  static constexpr int CTAS4 = 232448 / (smem(4) + 1024) < 4 ? 232448 / (smem(4) + 1024) : 4;
+  static constexpr int MAX_REGS = 65536 / (CTAS4 * 4 * 32);
+  __host__ __device__ static constexpr int ctas(int n) {
+    return min2(232448 / (smem(n) + 1024), 65536 / (MAX_REGS * 32 * n));
+  }
+  __host__ __device__ static constexpr int min2(int a, int b) { return a < b ? a : b; }
   static_assert(RING >= PART, "a warp's partial result reuses its ring");
+  static_assert(kWinWarps * C::STAGES * 8 <= BARS, "barriers");
 };
+
+// Warps per CTA and CTAs per (sequence, KV head).  A CTA's time is about that of
+// its prologue (length, block table, first rows: dependent loads, worth four
+// steps) and its warps' steps; a grid's is that times its waves of resident
+// CTAs, and a second wave is often nearly empty.  So the shape with the least
+// waves * (4 + steps) is taken.  Measured on 64 sequences x 8 KV heads, window 1024
+// (512 pairs), CTAs of 4 warps were 1.15 waves over an E4M3 cache, 43 us, and
+// clusters of 2, 4 and 8 at 8 sequences took 10.4 us (4 CTAs, one wave) and
+// 16.4 us (8 CTAs, 1.7 waves).
+struct WinShape {
+  int warps, cluster;
+};
+
+template <int D, bool FP8>
+inline WinShape win_shape(long long pairs, int max_chunks, int sms) {
+  using W = DecodeWinCfg<D, FP8>;
+  constexpr int NH = DecodeTmaCfg<D, FP8>::NH;
+  const WinShape shapes[] = {{4, 8}, {4, 4}, {4, 2}, {4, 1}, {3, 1}, {2, 1}, {1, 1}};
+  WinShape best = {4, 1};
+  long long least = 0;
+  for (const WinShape& s : shapes) {
+    const long long resident = (long long)W::ctas(s.warps) * sms;
+    const long long waves = (pairs * s.cluster + resident - 1) / resident;
+    const int warps = s.warps * s.cluster;
+    const long long steps = ((max_chunks + warps - 1) / warps + NH - 1) / NH;
+    const long long cost = waves * (4 + steps);
+    if (least == 0 || cost < least || (cost == least && warps < best.warps * best.cluster)) {
+      least = cost;
+      best = s;
+    }
+  }
+  return best;
+}
 
 // The tokens of chunk `t0 .. t0 + 15` that count, as a bit mask.
 __device__ __forceinline__ uint32_t win_chunk_mask(int t0, int lo, int len, int s_end) {
@@ -81,7 +121,7 @@ __device__ __forceinline__ float4 cluster_ld4(uint32_t addr) {
 }
 
 template <int D, bool FP8>
-__global__ void __launch_bounds__(kWinWarps * 32, 2) attn_decode_window_kernel(
+__global__ void __launch_bounds__(kWinWarps * 32, DecodeWinCfg<D, FP8>::CTAS4) attn_decode_window_kernel(
     const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
     const DecodeWindowParams wp) {
   using C = DecodeTmaCfg<D, FP8>;
@@ -93,13 +133,15 @@ __global__ void __launch_bounds__(kWinWarps * 32, 2) attn_decode_window_kernel(
   const uint32_t sbase = (raw_addr + 1023u) & ~1023u;
   uint8_t* sptr = smem_raw + (sbase - raw_addr);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int n_warps = blockDim.x >> 5;
+  const int off_bars = n_warps * W::RING, off_part = off_bars + W::BARS;
   const int cs = wp.cluster;
   const int rank = (int)(blockIdx.x % (unsigned)cs);
   const int pair = (int)(blockIdx.x / (unsigned)cs);
   const int kvh = pair % p.Hkv, b = pair / p.Hkv;
   const int hq0 = kvh * p.group;
   const uint32_t ring = sbase + warp * W::RING;
-  const uint32_t bars = sbase + W::OFF_BARS + warp * C::STAGES * 8;
+  const uint32_t bars = sbase + off_bars + warp * C::STAGES * 8;
 
   DecodeWarp<D, FP8> w;
   uint32_t qraw[D / 8];
@@ -113,8 +155,8 @@ __global__ void __launch_bounds__(kWinWarps * 32, 2) attn_decode_window_kernel(
   const int gap = max(lo / 16, ns) - ns;
   const int n_all = max((len + 15) / 16 - gap, 0);
   // this warp's run of it, whole steps
-  const int share = ((n_all + cs * kWinWarps - 1) / (cs * kWinWarps) + NH - 1) / NH * NH;
-  const int c_begin = min((rank * kWinWarps + warp) * share, n_all);
+  const int share = ((n_all + cs * n_warps - 1) / (cs * n_warps) + NH - 1) / NH * NH;
+  const int c_begin = min((rank * n_warps + warp) * share, n_all);
   const int c_end = min(c_begin + share, n_all);
   auto chunk_token = [&](int c) { return 16 * (c < ns ? c : c + gap); };
 
@@ -235,14 +277,14 @@ __global__ void __launch_bounds__(kWinWarps * 32, 2) attn_decode_window_kernel(
   __syncthreads();
   // ---- the CTA's part
   {
-    float* out = reinterpret_cast<float*>(sptr + W::OFF_PART_A);
+    float* out = reinterpret_cast<float*>(sptr + off_part);
     auto part = [&](int i) { return reinterpret_cast<const float*>(sptr + i * W::RING); };
-    for (int e = threadIdx.x * 4; e < p.group * D; e += kWinWarps * 32 * 4) {
+    for (int e = threadIdx.x * 4; e < p.group * D; e += blockDim.x * 4) {
       const int h = e / D;
       float m[kWinWarps], mx = -INFINITY;
 #pragma unroll
       for (int i = 0; i < kWinWarps; ++i) {
-        m[i] = part(i)[8 * D + h];
+        m[i] = i < n_warps ? part(i)[8 * D + h] : -INFINITY;
         mx = fmaxf(mx, m[i]);
       }
       float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -270,9 +312,9 @@ __global__ void __launch_bounds__(kWinWarps * 32, 2) attn_decode_window_kernel(
   cluster_sync();
   // ---- the result: the cluster's CTAs share its elements
   {
-    const uint32_t local = sbase + W::OFF_PART_A;
-    const int n_threads = cs * kWinWarps * 32;
-    for (int e = (rank * kWinWarps * 32 + (int)threadIdx.x) * 4; e < p.group * D;
+    const uint32_t local = sbase + off_part;
+    const int n_threads = cs * blockDim.x;
+    for (int e = (rank * (int)blockDim.x + (int)threadIdx.x) * 4; e < p.group * D;
          e += n_threads * 4) {
       const int h = e / D;
       float m[8], mx = -INFINITY;

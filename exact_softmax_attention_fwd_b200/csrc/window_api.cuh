@@ -16,20 +16,17 @@ int launch_decode_window(const CUtensorMap& mk, const CUtensorMap& mv, DecodeWin
   using W = DecodeWinCfg<D, FP8>;
   auto kern = attn_decode_window_kernel<D, FP8>;
   static std::atomic<unsigned long long> smem_set{0};
-  if (!set_smem_once(kern, W::SMEM, smem_set)) return ATTN_ERR_CUDA;
+  if (!set_smem_once(kern, W::smem(kWinWarps), smem_set)) return ATTN_ERR_CUDA;
   const int sms = sm_count();
   if (sms <= 0) return ATTN_ERR_CUDA;
-  // CTAs per (sequence, KV head): doubled while the grid leaves room for more
-  // (two CTAs an SM) and every warp keeps a step of its own
   const long long pairs = (long long)p.f.d.B * p.f.d.Hkv;
-  int cs = 1;
-  while (cs < 8 && pairs * cs < 2ll * sms && 2 * cs * kWinWarps * DecodeTmaCfg<D, FP8>::NH <= max_chunks)
-    cs *= 2;
+  const WinShape shape = win_shape<D, FP8>(pairs, max_chunks, sms);
+  const int cs = shape.cluster;
   p.cluster = cs;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(pairs * cs));
-  cfg.blockDim = dim3(kWinWarps * 32);
-  cfg.dynamicSmemBytes = W::SMEM;
+  cfg.blockDim = dim3(shape.warps * 32);
+  cfg.dynamicSmemBytes = W::smem(shape.warps);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
