@@ -200,6 +200,12 @@ __device__ __forceinline__ bool prefill_block_on(const PrefillParams& p, int b, 
                                kb)) != 0;
 }
 
+// A unit whose window leaves a gap behind a few first tokens computes only this
+// many columns of their tile: S = Q K^T with N = 32, P of 32 columns, P V over
+// 32 keys, instead of 128 of each.  (Typically 4 tokens are kept; the whole tile
+// costs a unit of window 1024 a tenth of its time.)
+constexpr int kSinkCols = 32;
+
 // One work unit: query rows [256*qb, 256*qb + 256) of head hq in sequence b.
 struct PrefillUnit {
   int qb, hq, b;
@@ -219,6 +225,7 @@ struct PrefillUnit {
   // kv_end, kv_first, kv_last above are stream positions.  Otherwise both are 0
   // and stream positions are key tiles.
   int sink_tiles, gap;
+  bool narrow;  // stream position 0 holds at most kSinkCols first tokens and nothing else seen
   __device__ __forceinline__ int key_tile(int x) const { return x < sink_tiles ? x : x + gap; }
 };
 
@@ -320,6 +327,7 @@ __device__ __forceinline__ bool prefill_unit(const PrefillParams& p, int k, Pref
   }
   if (u.kv_last == 0) u.kv_first = 0;
   u.sink_tiles = u.gap = 0;
+  u.narrow = false;
   if (MASKS && p.sinks > 0 && u.kv_last > 0) {
     // Both query tiles walk the whole stream from its start: where their
     // windows begin a tile apart, the later one meets one tile that it does
@@ -328,6 +336,7 @@ __device__ __forceinline__ bool prefill_unit(const PrefillParams& p, int k, Pref
     if (u.kv_first > st) {
       u.sink_tiles = st;
       u.gap = u.kv_first - st;
+      u.narrow = p.sinks <= kSinkCols;
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -612,24 +621,28 @@ __global__ void __launch_bounds__(384, 1)
         const bool r = mbar_wait_slow(b, ph, abort_flag);
         return __all_sync(0xffffffffu, r);
       };
-      auto issue_qk = [&](int i, int stage) {
+      constexpr uint32_t idesc_qk_sink = idesc_bf16_f32(128, kSinkCols, false);
+      auto issue_qk = [&](int i, int stage, bool narrow = false) {
         const uint64_t qd = smem_desc_sw128(opaque_u32(sbase + C::OFF_Q + i * C::TILE_BYTES), 16, 1024);
         const uint64_t kd = smem_desc_sw128(opaque_u32(sbase + C::OFF_K + stage * C::TILE_BYTES), 16, 1024);
         const uint32_t dt = tmem + C::tmem_s(i);
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
           const uint64_t off = (uint64_t)(((ks >> 2) * C::CB_BYTES + (ks & 3) * 32) >> 4);
-          umma_ss(dt, qd + off, kd + off, idesc_qk, ks > 0 ? 1u : 0u);
+          umma_ss(dt, qd + off, kd + off, MASKS && narrow ? idesc_qk_sink : idesc_qk,
+                  ks > 0 ? 1u : 0u);
         }
       };
-      auto issue_pv = [&](int i, int stage, bool accumulate) {
+      auto issue_pv = [&](int i, int stage, bool accumulate, bool narrow = false) {
         const uint64_t vd = smem_desc_sw128(opaque_u32(sbase + C::OFF_V + stage * C::TILE_BYTES), C::CB_BYTES, 1024);
         const uint32_t ts = opaque_u32(tmem + C::tmem_s(i));
         const uint32_t dt = tmem + C::tmem_o(i);
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks)
+        for (int ks = 0; ks < 8; ++ks) {
+          if (MASKS && narrow && ks >= kSinkCols / 16) break;
           umma_ts(dt, ts + ks * 8, vd + (uint64_t)((ks * 2048) >> 4), idesc_pv,
                   (accumulate || ks > 0) ? 1u : 0u);
+        }
       };
       uint32_t kv = 0;                  // ring position
       uint32_t q_waits0 = 0, q_waits1 = 0;  // Q_FULL phases consumed per tile slot
@@ -651,7 +664,7 @@ __global__ void __launch_bounds__(384, 1)
             ++qw;
             tc_fence_after_sync();
             if (elect_one()) {
-              issue_qk(i, s);
+              issue_qk(i, s, u.narrow);
               umma_commit(bar(C::B_SFULL + i));
               if (u.kv_end[i] == jb + 1) umma_commit(bar(C::B_QFREE + i));
             }
@@ -763,7 +776,7 @@ __global__ void __launch_bounds__(384, 1)
               k_next = true;
             }
             if (elect_one()) {
-              issue_pv(i, s, j > b0);
+              issue_pv(i, s, j > b0, u.narrow && j == jb);
               if (more) {
                 issue_qk(i, s1);
                 umma_commit(bar(C::B_SFULL + i));
@@ -845,6 +858,42 @@ __global__ void __launch_bounds__(384, 1)
         if (!(ok = mbar_wait_warp(bar(C::B_SFULL + i), s_waits & 1u, abort_flag))) break;
         ++s_waits;
         tc_fence_after_sync();
+        if (MASKS && u.narrow && j == kb) {
+          // the first tokens' columns alone; nothing has been accumulated yet, so
+          // this sets the base and the sums
+          uint32_t x[32];
+          tmem_ld32_sync(t_s, x);
+          const uint32_t vis = low_bits(p.sinks);
+          float mx = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < kSinkCols; ++c) {
+            float v = __uint_as_float(x[c]);
+            if (!scale_pos) v *= p.scale_log2;
+            if (!(vis & (1u << c))) v = -INFINITY;
+            x[c] = __float_as_uint(v);
+            mx = fmaxf(mx, v);
+          }
+          m_run = mx * c2;
+          const float base = (m_run == -INFINITY) ? 0.f : m_run;
+          uint32_t pk[kSinkCols / 2];
+          float l0 = 0.f, l1 = 0.f, r0 = 0.f, r1 = 0.f;
+#pragma unroll
+          for (int c = 0; c < kSinkCols / 2; ++c) {
+            const float p0 = ex2(fmaf(__uint_as_float(x[2 * c]), c2, -base));
+            const float p1 = ex2(fmaf(__uint_as_float(x[2 * c + 1]), c2, -base));
+            pk[c] = pack_bf16x2(p0, p1);
+            l0 += p0;
+            l1 += p1;
+            add_bf16x2_halves(pk[c], r0, r1);
+          }
+          tmem_st16(t_s, pk);
+          l_run = l0 + l1;
+          lr_run = r0 + r1;
+          tmem_st_wait();
+          tc_fence_before_sync();
+          mbar_arrive(bar(C::B_PFULL + i));
+          continue;
+        }
         float s[128];
         {
           uint32_t u0[32], u1[32], u2[32], u3[32];
