@@ -32,6 +32,7 @@ from ._binding import (  # noqa: F401
     attn_fwd_paged_fp8,
     attn_fwd_paged_fp8_workspace_size,
     attn_fwd_paged_window,
+    attn_fwd_paged_window_workspace_size,
     attn_fwd_varlen,
     attn_fwd_varlen_workspace_size,
     attn_fwd_window,

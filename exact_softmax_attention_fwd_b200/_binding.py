@@ -72,6 +72,7 @@ SIGNATURES = {
     "attn_fwd_window_sinks": (_I, [_P] * 5 + [_I] * 6 + [_F, _P, _I, _I, _P]),
     "attn_fwd_paged_window": (_I, [_P] * 6 + [_I] * 4 + [_LL] + [_I] * 4 + [_F, _I, _I, _P, _P, _P,
                                                                            _SZ, _P]),
+    "attn_fwd_paged_window_workspace_size": (_SZ, [_I, _I, _I, _LL, _I]),
     "attn_bwd_window_sinks_workspace_size": (_SZ, [_I] * 8),
     "attn_bwd_window_sinks": (_I, [_P] * 9 + [_I] * 6 + [_F, _P, _I, _I, _P, _SZ, _P]),
     "attn_decode_paged_window": (_I, [_P] * 5 + [_I] * 7 + [_F, _I, _I, _P, _P, _P]),
@@ -1042,6 +1043,12 @@ def attn_bwd_window_sinks(q, k, v, o, lse, d_o, scale: float, window: int, sinks
     return dq, dk, dv
 
 
+def attn_fwd_paged_window_workspace_size(B: int, Hq: int, Hkv: int, total_q: int,
+                                         max_seqlen_q: int) -> int:
+    return int(load_library().attn_fwd_paged_window_workspace_size(B, Hq, Hkv, total_q,
+                                                                   max_seqlen_q))
+
+
 def attn_fwd_paged_window(q, k_cache, v_cache, block_table, cu_seqlens_q, seq_lens_k,
                           max_seqlen_q: int, scale: float, window: int, sinks: int = 0, out=None,
                           lse=None, workspace=None, return_lse: bool = True, stream=None):
@@ -1067,7 +1074,7 @@ def attn_fwd_paged_window(q, k_cache, v_cache, block_table, cu_seqlens_q, seq_le
     out = _buffer(out, q, qs, bf16, stream, "out")
     if lse is not None or return_lse:
         lse = _buffer(lse, q, (Hq, total), torch.float32, stream, "lse")
-    need = attn_fwd_varlen_workspace_size(B, total, max_seqlen_q)
+    need = attn_fwd_paged_window_workspace_size(B, Hq, cache[2], total, max_seqlen_q)
     ws, ws_bytes, workspace = _workspace(workspace, q, need, stream)
     _launch("attn_fwd_paged_window", index, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
             block_table.data_ptr(), cu_seqlens_q.data_ptr(), seq_lens_k.data_ptr(), cache[1], B,

@@ -128,17 +128,17 @@ bool make_tile_map(CUtensorMap* map, const void* ptr, int D, long long rows, lon
 }
 
 // 3-D bf16 map over a packed token-major [tokens, heads, D] tensor, box =
-// box_rows tokens of one head x 64 columns, 128-byte swizzle: with 128 rows the
+// box_rows tokens of box_heads heads (one, unless said) x 64 columns, 128-byte swizzle: with 128 rows the
 // same shared-memory tile as make_tile_map gives (128 rows of 128 bytes); a
 // paged pool [num_pages, page_size, heads, D] is such a tensor with
 // num_pages * page_size tokens, read one page (box_rows = page_size) at a time.
 bool make_token_map(CUtensorMap* map, const void* ptr, int D, long long heads, long long tokens,
-                    unsigned box_rows = 128) {
-  const MapKey key{ptr, 1, D, heads, tokens, box_rows};
+                    unsigned box_rows = 128, unsigned box_heads = 1) {
+  const MapKey key{ptr, 1, D, heads, tokens, box_rows + (box_heads << 16)};
   if (map_cache().find(key, map)) return true;
   const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)tokens};
   const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)heads * D * 2};
-  const cuuint32_t box[3] = {64, 1, box_rows};
+  const cuuint32_t box[3] = {64, box_heads, box_rows};
   if (!encode_3d(map, ptr, dims, strides, box)) return false;
   map_cache().put(key, *map);
   return true;
@@ -507,10 +507,10 @@ int paged_prefill_run(const void* q, const void* k_cache, const void* v_cache,
                       const int32_t* seq_lens_k, int page_size, int B, int Hq, int Hkv,
                       long long total_q, int max_seqlen_q, int max_pages_per_seq, int num_pages,
                       int d, int causal, float scale, void* o, float* lse, void* workspace,
-                      cudaStream_t stream, int window = 0, int sinks = 0) {
+                      cudaStream_t stream, int window = 0, int sinks = 0, int pack = 0) {
   int* unit_count = static_cast<int*>(workspace);
   int2* units = reinterpret_cast<int2*>(static_cast<char*>(workspace) + 16);
-  const long long max_units = varlen_max_units(B, total_q);
+  const long long max_units = varlen_max_units(B, total_q << pack);
   const int max_keys = max_pages_per_seq * page_size;
   int shift, n_levels;
   varlen_levels(max_keys, shift, n_levels);
@@ -518,10 +518,10 @@ int paged_prefill_run(const void* q, const void* k_cache, const void* v_cache,
   if (!schedule_smem_ready()) return ATTN_ERR_CUDA;
   attn_varlen_schedule_kernel<<<1, 1024, sched_smem, stream>>>(
       cu_seqlens_q, nullptr, seq_lens_k, B, (int)total_q, 0, max_seqlen_q, max_keys, causal,
-      window, 0, shift, n_levels, units, unit_count, (int)max_units);
+      window, 0, shift, n_levels, units, unit_count, (int)max_units, pack);
   if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
   CUtensorMap mq, mk, mv;
-  if (!make_token_map(&mq, q, d, Hq, total_q) ||
+  if (!make_token_map(&mq, q, d, Hq, total_q, 128 >> pack, 1u << pack) ||
       !make_token_map(&mk, k_cache, d, Hkv, (long long)num_pages * page_size, page_size) ||
       !make_token_map(&mv, v_cache, d, Hkv, (long long)num_pages * page_size, page_size))
     return ATTN_ERR_CUDA;
@@ -547,6 +547,7 @@ int paged_prefill_run(const void* q, const void* k_cache, const void* v_cache,
     prm.window = window;
     prm.sinks = sinks;
     prm.v_pool = static_cast<const uint16_t*>(v_cache);
+    prm.pack = pack;
     return d == 128
                ? launch_prefill<128, true, kLayoutPaged, true>(mq, mk, mv, mq, prm, stream, max_units)
                : launch_prefill<64, true, kLayoutPaged, true>(mq, mk, mv, mq, prm, stream, max_units);
@@ -1094,7 +1095,7 @@ int attn_fwd_varlen(const void* q, const void* k, const void* v, void* o, float*
   if (!schedule_smem_ready()) return ATTN_ERR_CUDA;
   attn_varlen_schedule_kernel<<<1, 1024, sched_smem, stream>>>(
       cu_seqlens_q, cu_seqlens_k, nullptr, B, (int)total_q, (int)total_k, max_seqlen_q, 0, causal,
-      0, 0, shift, n_levels, units, unit_count, (int)max_units);
+      0, 0, shift, n_levels, units, unit_count, (int)max_units, 0);
   if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
   // 2. the prefill kernel over packed token-major tensors
   CUtensorMap mq, mk, mv;

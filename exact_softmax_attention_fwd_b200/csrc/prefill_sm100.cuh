@@ -102,6 +102,11 @@ struct PrefillParams {
   const int* block_table;   // [B, max_pages]
   int max_pages, page_size, num_pages;
   const uint16_t* v_pool;   // the V pool itself (masked paged launches: tail pages)
+  // masked paged launches: the 2^pack query heads of a KV head as rows of one
+  // tile, row r of a sequence being token r >> pack of head r & (2^pack - 1).
+  // A chunk of a few tokens then fills a tile with all heads of a group instead
+  // of a small part of one tile per head.
+  int pack;
   const int2* units;    // (sequence, query block), heaviest first
   const int* unit_count;
   int total_q;
@@ -172,12 +177,15 @@ constexpr int kLayoutPaged = 2;
 // otherwise; tiles outside the union over the tile's rows are skipped whole
 // ("Attention Kernel", section "可编程 mask": block-level skipping, then an
 // element-wise rule inside the tiles left).
+// Rows are query rows, 2^pack to a token.
 __device__ __forceinline__ void prefill_kv_range(int row0, int Sq, int klen, bool causal,
-                                                 int window, int prefix, int& lo, int& hi) {
+                                                 int window, int prefix, int& lo, int& hi,
+                                                 int pack = 0) {
   lo = hi = 0;
   if (row0 >= Sq) return;
-  const long long off = (long long)klen - Sq;
-  const int last_row = min(row0 + 127, Sq - 1);
+  const long long off = (long long)klen - (Sq >> pack);
+  const int last_row = min(row0 + 127, Sq - 1) >> pack;
+  row0 >>= pack;
   long long top = (long long)klen - 1;  // largest key any row of the tile sees
   long long bot = 0;                    // smallest
   if (causal) {
@@ -242,17 +250,19 @@ template <bool CAUSAL, int LAYOUT, bool MASKS>
 __device__ __forceinline__ bool prefill_unit(const PrefillParams& p, int k, PrefillUnit& u,
                                              const uint16_t* sched = nullptr) {
   constexpr bool VARLEN = LAYOUT != kLayoutDense;
+  constexpr bool PACKS = MASKS && LAYOUT == kLayoutPaged;
   const long long G = gridDim.x;
   const long long c = blockIdx.x;
   const long long r = (long long)k * G + ((k & 1) ? (G - 1 - c) : c);
   if (VARLEN) {
-    if (r >= (long long)__ldg(p.unit_count) * p.Hq) return false;
-    const int2 e = __ldg(&p.units[r / p.Hq]);
-    u.hq = (int)(r % p.Hq);
+    const int heads = PACKS ? p.Hq >> p.pack : p.Hq;  // runs of heads that are units of their own
+    if (r >= (long long)__ldg(p.unit_count) * heads) return false;
+    const int2 e = __ldg(&p.units[r / heads]);
+    u.hq = (int)(r % heads) << (PACKS ? p.pack : 0);
     u.b = e.x;
     u.qb = e.y;
     u.q_tok0 = __ldg(p.cu_q + u.b);
-    u.sq = __ldg(p.cu_q + u.b + 1) - u.q_tok0;  // listed sequences passed the
+    u.sq = (__ldg(p.cu_q + u.b + 1) - u.q_tok0) << (PACKS ? p.pack : 0);  // listed sequences passed the
     if (LAYOUT == kLayoutPaged) {                  // schedule kernel's checks
       u.k_tok0 = 0;
       u.klen = __ldg(p.seq_lens_k + u.b);
@@ -310,7 +320,7 @@ __device__ __forceinline__ bool prefill_unit(const PrefillParams& p, int k, Pref
     u.hq_t[i] = pairs ? u.hq + i : u.hq;
     u.row0[i] = pairs ? u.qb * 128 : u.qb * 256 + i * 128;
     prefill_kv_range(u.row0[i], u.sq, u.klen, CAUSAL, MASKS ? p.window : 0,
-                     MASKS ? p.prefix : 0, u.kv_begin[i], u.kv_end[i]);
+                     MASKS ? p.prefix : 0, u.kv_begin[i], u.kv_end[i], PACKS ? p.pack : 0);
     if (MASKS && p.block_mask != nullptr) {
       // tighten the range to its first and last computed block, so that a
       // tile with no block left has an empty range (and no Q load)
@@ -360,6 +370,7 @@ __global__ void __launch_bounds__(384, 1)
   using C = PrefillCfg<D>;
   constexpr bool VARLEN = LAYOUT != kLayoutDense;
   constexpr bool PAGED = LAYOUT == kLayoutPaged;
+  const int pack = MASKS && PAGED ? p.pack : 0;  // see PrefillParams
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   const uint32_t sbase = (raw_addr + 1023u) & ~1023u;
@@ -466,7 +477,7 @@ __global__ void __launch_bounds__(384, 1)
         for (int cb = 0; cb < C::NCB; ++cb)
           tma_load_3d(sbase + C::OFF_Q + i * C::TILE_BYTES + cb * C::CB_BYTES, &tm_q,
                       bar(C::B_QFULL + i), 64 * cb, VARLEN ? u.hq : u.row0[i],
-                      VARLEN ? u.q_tok0 + u.row0[i] : u.b * p.Hq + u.hq_t[i]);
+                      VARLEN ? u.q_tok0 + (u.row0[i] >> pack) : u.b * p.Hq + u.hq_t[i]);
         ++n;
         return true;
       };
@@ -835,16 +846,17 @@ __global__ void __launch_bounds__(384, 1)
       // visible keys of this row: [lo_row, hi_row]; a tile needs the per-element
       // rule unless every row of it sees all of it (j*128 >= lo_tile and
       // j*128 + 127 <= hi_tile, the tightest bounds over its rows)
-      const long long koff = (long long)u.klen - u.sq;
-      const int last_row = min(row0 + 127, u.sq - 1);
+      const long long koff = (long long)u.klen - (u.sq >> pack);
+      const int last_row = min(row0 + 127, u.sq - 1) >> pack;  // as tokens, like the two below
+      const int tok_row = row >> pack, tok_row0 = row0 >> pack;
       long long hi_row = (long long)u.klen - 1, hi_tile = hi_row;
       long long lo_row = 0, lo_tile = 0;
       const int prefix = MASKS ? p.prefix : 0, window = MASKS ? p.window : 0;
       if (CAUSAL) {
-        hi_row = min(hi_row, max((long long)row + koff, (long long)prefix - 1));
-        hi_tile = min(hi_tile, max((long long)row0 + koff, (long long)prefix - 1));
+        hi_row = min(hi_row, max((long long)tok_row + koff, (long long)prefix - 1));
+        hi_tile = min(hi_tile, max((long long)tok_row0 + koff, (long long)prefix - 1));
         if (window > 0) {
-          lo_row = max(0LL, (long long)row + koff - window + 1);
+          lo_row = max(0LL, (long long)tok_row + koff - window + 1);
           lo_tile = max(0LL, (long long)last_row + koff - window + 1);
         }
       }
@@ -1036,8 +1048,9 @@ __global__ void __launch_bounds__(384, 1)
             for (int e = 0; e < 32; ++e) v[c][e] = 0u;
         }
         if (row < u.sq) {
-          const size_t tok = (size_t)u.q_tok0 + row;
-          uint4* dst = reinterpret_cast<uint4*>(p.o + (tok * p.Hq + u.hq) * D);
+          const size_t tok = (size_t)u.q_tok0 + tok_row;
+          const int head = u.hq + (row & ((1 << pack) - 1));
+          uint4* dst = reinterpret_cast<uint4*>(p.o + (tok * p.Hq + head) * D);
 #pragma unroll
           for (int q8 = 0; q8 < D / 8; ++q8) {  // 8 bf16 = 16 bytes per store
             const uint32_t* x = &v[q8 >> 2][(q8 & 3) * 8];
@@ -1050,7 +1063,7 @@ __global__ void __launch_bounds__(384, 1)
           }
           if (p.lse != nullptr) {
             const float lse = (l_run > 0.f) ? (m_run + lg2(l_run)) * 0.69314718055994531f : -INFINITY;
-            p.lse[(size_t)u.hq * p.total_q + tok] = lse;
+            p.lse[(size_t)head * p.total_q + tok] = lse;
           }
         }
       } else {

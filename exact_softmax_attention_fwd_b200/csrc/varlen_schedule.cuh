@@ -51,14 +51,15 @@ __device__ __forceinline__ bool varlen_seq_lengths(const int* cu_q, const int* c
   return !bad;
 }
 
-// 128-key tiles the two query tiles of block qb visit (prefill_kv_range).
+// 128-key tiles the two query tiles of block qb visit (prefill_kv_range); len_q
+// counts rows, 2^pack to a token.
 __device__ __forceinline__ int varlen_unit_weight(int qb, int len_q, int len_k, bool causal,
-                                                  int window, int prefix) {
+                                                  int window, int prefix, int pack) {
   int w = 0;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     int lo, hi;
-    prefill_kv_range(qb * 256 + i * 128, len_q, len_k, causal, window, prefix, lo, hi);
+    prefill_kv_range(qb * 256 + i * 128, len_q, len_k, causal, window, prefix, lo, hi, pack);
     w += hi - lo;
   }
   return w;
@@ -108,7 +109,7 @@ __global__ void __launch_bounds__(1024, 1)
                                 int total_q, int total_k, int max_seqlen_q, int max_keys,
                                 int causal, int window, int prefix, int level_shift,
                                 int n_levels, int2* units,
-                                int* unit_count, int max_units) {
+                                int* unit_count, int max_units, int pack) {
   extern __shared__ int sh[];
   int* lev = sh;                  // counts, then first positions / cursors
   int* cnt_copy = sh + n_levels;  // counts kept for the total
@@ -120,8 +121,10 @@ __global__ void __launch_bounds__(1024, 1)
     if (!varlen_seq_lengths(cu_q, cu_k, seq_lens_k, b, total_q, total_k, max_seqlen_q, max_keys,
                             lq, lk))
       continue;
+    lq <<= pack;
     for (int qb = 0; qb * 256 < lq; ++qb) {
-      const int L = min(varlen_unit_weight(qb, lq, lk, causal != 0, window, prefix) >> level_shift, n_levels - 1);
+      const int L = min(varlen_unit_weight(qb, lq, lk, causal != 0, window, prefix, pack) >> level_shift,
+                        n_levels - 1);
       atomicAdd(&lev[L], 1);
     }
   }
@@ -140,8 +143,10 @@ __global__ void __launch_bounds__(1024, 1)
     if (!varlen_seq_lengths(cu_q, cu_k, seq_lens_k, b, total_q, total_k, max_seqlen_q, max_keys,
                             lq, lk))
       continue;
+    lq <<= pack;
     for (int qb = 0; qb * 256 < lq; ++qb) {
-      const int L = min(varlen_unit_weight(qb, lq, lk, causal != 0, window, prefix) >> level_shift, n_levels - 1);
+      const int L = min(varlen_unit_weight(qb, lq, lk, causal != 0, window, prefix, pack) >> level_shift,
+                        n_levels - 1);
       const int pos = atomicAdd(&lev[L], 1);
       if (pos < max_units) units[pos] = make_int2(b, qb);
     }

@@ -10,6 +10,16 @@
 namespace attn_b200 {
 namespace {
 
+// Query heads of a KV head that share a tile of the paged kernel, as a power of
+// two (0: each head has tiles of its own): all of a group's, when they are 2, 4,
+// 8 or 16.
+int window_pack(int Hq, int Hkv) {
+  const int group = Hq / Hkv;
+  for (int s = 1; s <= 4; ++s)
+    if (group == 1 << s) return s;
+  return 0;
+}
+
 template <int D, bool FP8>
 int launch_decode_window(const CUtensorMap& mk, const CUtensorMap& mv, DecodeWindowParams& p,
                          int max_chunks, cudaStream_t stream) {
@@ -156,6 +166,14 @@ int attn_bwd_window_sinks(const void* q, const void* k, const void* v, const voi
                    window, 0, nullptr, 1, workspace, workspace_bytes, stream, sinks);
 }
 
+size_t attn_fwd_paged_window_workspace_size(int B, int Hq, int Hkv, long long total_q,
+                                            int max_seqlen_q) {
+  if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || total_q < 0 || total_q > 0x7fffffffLL ||
+      max_seqlen_q < 1 || max_seqlen_q > kVarlenMaxLevels * 256)
+    return 0;
+  return 16 + 8 * (size_t)varlen_max_units(B, total_q << window_pack(Hq, Hkv));
+}
+
 int attn_fwd_paged_window(const void* q, const void* k_cache, const void* v_cache,
                           const int32_t* block_table, const int32_t* cu_seqlens_q,
                           const int32_t* seq_lens_k, int page_size, int B, int Hq, int Hkv,
@@ -168,7 +186,7 @@ int attn_fwd_paged_window(const void* q, const void* k_cache, const void* v_cach
                                           max_pages_per_seq, num_pages, d, 1, scale, o, lse);
   if (st != ATTN_OK) return st;
   if (window < 0 || sinks < 0) return ATTN_ERR_INVALID_ARG;
-  const size_t need = attn_fwd_varlen_workspace_size(B, total_q, max_seqlen_q);
+  const size_t need = attn_fwd_paged_window_workspace_size(B, Hq, Hkv, total_q, max_seqlen_q);
   if (workspace == nullptr || workspace_bytes < need) return ATTN_ERR_WORKSPACE;
   if (!aligned16(workspace)) return ATTN_ERR_ALIGNMENT;
   if (total_q == 0) return ATTN_OK;
@@ -177,7 +195,8 @@ int attn_fwd_paged_window(const void* q, const void* k_cache, const void* v_cach
   return paged_prefill_run(q, k_cache, v_cache, block_table, cu_seqlens_q, seq_lens_k, page_size,
                            B, Hq, Hkv, total_q, max_seqlen_q, max_pages_per_seq, num_pages, d, 1,
                            scale, o, lse, workspace, reinterpret_cast<cudaStream_t>(stream),
-                           window > 0 ? window : INT_MAX, window > 0 ? sinks : 0);
+                           window > 0 ? window : INT_MAX, window > 0 ? sinks : 0,
+                           window_pack(Hq, Hkv));
 }
 
 }  // extern "C"

@@ -679,14 +679,22 @@ int attn_fwd_window_sinks(const void* q, const void* k, const void* v, void* o, 
                           const int32_t* k_lens, int window, int sinks, attn_stream_t stream);
 
 /*
+ * attn_fwd_paged_window_workspace_size -- bytes of device workspace that
+ * attn_fwd_paged_window needs (its list of work units).  0 for invalid arguments.
+ */
+size_t attn_fwd_paged_window_workspace_size(int B, int Hq, int Hkv, long long total_q,
+                                            int max_seqlen_q);
+
+/*
  * attn_fwd_paged_window -- attn_fwd_paged (causal) with a sliding window and
  * visible first tokens, masked as attn_fwd_window_sinks with k_len =
  * seq_lens_k[b] and Sq the sequence's query tokens.  Pages that lie wholly
  * between the first tokens and the windows of a block of query rows are not
  * read.  Slots behind a sequence's end may hold anything (a cache whose last
  * page was never filled); the slots in use must be finite.
- * Other arguments, layouts, workspace, device-side checks and errors as
- * attn_fwd_paged (INVALID_ARG also for a negative window or sinks).
+ *   workspace: attn_fwd_paged_window_workspace_size(...) bytes, 16-byte aligned.
+ * Other arguments, layouts, device-side checks and errors as attn_fwd_paged
+ * (INVALID_ARG also for a negative window or sinks).
  */
 int attn_fwd_paged_window(const void* q, const void* k_cache, const void* v_cache,
                           const int32_t* block_table, const int32_t* cu_seqlens_q,

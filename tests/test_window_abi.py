@@ -69,7 +69,7 @@ def test_backward_workspace(lib):
 def _paged(lib, q=FAKE, kc=FAKE, tbl=FAKE, page=16, B_=2, total=50, maxq=30, d=128, window=16,
            sinks=4, ws=FAKE, ws_bytes=None):
     if ws_bytes is None:
-        ws_bytes = lib.attn_fwd_varlen_workspace_size(B_, total, maxq) if B_ > 0 else 0
+        ws_bytes = lib.attn_fwd_paged_window_workspace_size(B_, 4, 2, total, maxq) if B_ > 0 else 0
     return lib.attn_fwd_paged_window(q, kc, FAKE, tbl, FAKE, FAKE, page, B_, 4, 2, total, maxq, 8, 20,
                                      d, 0.1, window, sinks, FAKE, None, ws, ws_bytes, None)
 
@@ -83,6 +83,16 @@ def _paged(lib, q=FAKE, kc=FAKE, tbl=FAKE, page=16, B_=2, total=50, maxq=30, d=1
     (dict(ws_bytes=8), B.ATTN_ERR_WORKSPACE)])
 def test_paged_validation(lib, kw, status):
     assert _paged(lib, **kw) == status
+
+
+def test_paged_workspace(lib):
+    size = lib.attn_fwd_paged_window_workspace_size
+    # the unit list: a 16-byte header and 8 bytes for each possible unit of 256 rows
+    assert size(3, 4, 4, 1000, 512) == 16 + 8 * (1000 // 256 + 4)
+    assert size(3, 8, 2, 1000, 512) == 16 + 8 * (4000 // 256 + 4)     # a group's heads as rows
+    assert size(3, 6, 2, 1000, 512) == 16 + 8 * (1000 // 256 + 4)     # groups of 3: not
+    for bad in ((0, 4, 2, 10, 10), (1, 4, 3, 10, 10), (1, 4, 2, -1, 10), (1, 4, 2, 10, 0)):
+        assert size(*bad) == 0
 
 
 def test_paged_without_tokens_launches_nothing(lib):

@@ -152,6 +152,9 @@ PAGED = [
     ([130, 600], [1400, 600], 3, 1, 64, 64, 37, 140),
     ([257, 5], [257, 129], 4, 4, 128, 128, 64, 1),
     ([20, 20], [20, 400], 2, 2, 64, 32, 0, 3),             # no window
+    ([1, 33, 200, 64, 7], [700, 33, 450, 64, 2000], 8, 1, 128, 16, 90, 4),   # 8 heads to a tile
+    ([1, 9, 140], [40, 700, 300], 16, 1, 64, 64, 50, 33),  # 16
+    ([31, 65], [400, 65], 12, 2, 128, 32, 64, 4),          # 6: tiles of one head
     ([5, 9], [3, 9], 2, 1, 64, 16, 4, 2),                  # more queries than keys: empty rows
 ]
 
