@@ -2,10 +2,10 @@
 
 Tolerance, element by element: the result is rounded to bf16 once (half a step,
 2^-8 of the value), after an fp32 rotation whose errors scale with |a| + |b| of
-the pair: the remainder of the turns is rounded to fp32 (at most 2^-26 turns,
-9.4e-8 radians), sine and cosine are good to 2 units in the last place
-(2.4e-7), the factor m, the two products and their sum round once each
-(4 x 2^-24): 5.8e-7 m (|a| + |b|) in all, taken as 1e-6.
+the pair: the remainder of the turns is good to 2^-33 and its radians, below pi,
+round to fp32 (pi 2^-24, 1.9e-7), the fast sine and cosine are good to 2^-21
+(4.8e-7) over [-pi, pi], the factor m, the two products and their sum round
+once each (4 x 2^-24): 9.1e-7 m (|a| + |b|) in all, taken as 1e-6.
 """
 import numpy as np
 import pytest
