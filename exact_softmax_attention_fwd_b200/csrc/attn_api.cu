@@ -52,55 +52,6 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-// A tensor map is a pure function of (address, sizes, strides, box, layout),
-// so encoded maps are kept in a small cache keyed by exactly those: repeated
-// calls on the same buffers (a serving loop, a benchmark) skip the encode.
-struct MapKey {
-  const void* ptr;
-  int kind;  // 0: [planes, rows, D] tiles; 1: token-major [tokens, heads, D]; 2, 3: E4M3 forms
-  int D;
-  long long a, b;  // rows, planes  |  heads, tokens
-  unsigned box_rows;
-  bool operator==(const MapKey& o) const {
-    return ptr == o.ptr && kind == o.kind && D == o.D && a == o.a && b == o.b &&
-           box_rows == o.box_rows;
-  }
-};
-
-class MapCache {
- public:
-  bool find(const MapKey& k, CUtensorMap* out) {
-    std::lock_guard<std::mutex> g(mu_);
-    for (int i = 0; i < kSize; ++i)
-      if (used_[i] && keys_[i] == k) {
-        *out = maps_[i];
-        return true;
-      }
-    return false;
-  }
-  void put(const MapKey& k, const CUtensorMap& m) {
-    std::lock_guard<std::mutex> g(mu_);
-    const int i = next_;
-    next_ = (next_ + 1) % kSize;
-    keys_[i] = k;
-    maps_[i] = m;
-    used_[i] = true;
-  }
-
- private:
-  static constexpr int kSize = 64;
-  std::mutex mu_;
-  MapKey keys_[kSize] = {};
-  CUtensorMap maps_[kSize] = {};
-  bool used_[kSize] = {};
-  int next_ = 0;
-};
-
-MapCache& map_cache() {
-  static MapCache c;
-  return c;
-}
-
 bool encode_3d(CUtensorMap* map, const void* ptr, const cuuint64_t dims[3],
                const cuuint64_t strides[2], const cuuint32_t box[3],
                CUtensorMapDataType dtype = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
@@ -117,31 +68,23 @@ bool encode_3d(CUtensorMap* map, const void* ptr, const cuuint64_t dims[3],
 // x 64 columns, 128-byte swizzle (the layout the tcgen05 descriptors expect).
 bool make_tile_map(CUtensorMap* map, const void* ptr, int D, long long rows, long long planes,
                    unsigned box_rows = 128) {
-  const MapKey key{ptr, 0, D, rows, planes, box_rows};
-  if (map_cache().find(key, map)) return true;
   const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)rows, (cuuint64_t)planes};
   const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)rows * D * 2};
   const cuuint32_t box[3] = {64, box_rows, 1};
-  if (!encode_3d(map, ptr, dims, strides, box)) return false;
-  map_cache().put(key, *map);
-  return true;
+  return encode_3d(map, ptr, dims, strides, box);
 }
 
 // 3-D bf16 map over a packed token-major [tokens, heads, D] tensor, box =
-// box_rows tokens of box_heads heads (one, unless said) x 64 columns, 128-byte swizzle: with 128 rows the
-// same shared-memory tile as make_tile_map gives (128 rows of 128 bytes); a
-// paged pool [num_pages, page_size, heads, D] is such a tensor with
+// box_rows tokens of box_heads heads (one, unless said) x 64 columns, 128-byte
+// swizzle: with 128 rows in all the same shared-memory tile as make_tile_map
+// gives (128 rows of 128 bytes); a paged pool [num_pages, page_size, heads, D] is such a tensor with
 // num_pages * page_size tokens, read one page (box_rows = page_size) at a time.
 bool make_token_map(CUtensorMap* map, const void* ptr, int D, long long heads, long long tokens,
                     unsigned box_rows = 128, unsigned box_heads = 1) {
-  const MapKey key{ptr, 1, D, heads, tokens, box_rows + (box_heads << 16)};
-  if (map_cache().find(key, map)) return true;
   const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)tokens};
   const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)heads * D * 2};
   const cuuint32_t box[3] = {64, box_heads, box_rows};
-  if (!encode_3d(map, ptr, dims, strides, box)) return false;
-  map_cache().put(key, *map);
-  return true;
+  return encode_3d(map, ptr, dims, strides, box);
 }
 
 // 3-D map over a paged E4M3 pool read as the token-major byte tensor
@@ -149,32 +92,22 @@ bool make_token_map(CUtensorMap* map, const void* ptr, int D, long long heads, l
 // 128-byte swizzle for 128-byte rows, 64-byte swizzle for 64-byte rows.
 bool make_token_map_u8(CUtensorMap* map, const void* ptr, int D, long long heads,
                        long long tokens) {
-  const MapKey key{ptr, 2, D, heads, tokens, 16u};
-  if (map_cache().find(key, map)) return true;
   const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)tokens};
   const cuuint64_t strides[2] = {(cuuint64_t)D, (cuuint64_t)heads * D};
   const cuuint32_t box[3] = {(cuuint32_t)D, 1, 16};
-  if (!encode_3d(map, ptr, dims, strides, box, CU_TENSOR_MAP_DATA_TYPE_UINT8,
-                 D >= 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
-    return false;
-  map_cache().put(key, *map);
-  return true;
+  return encode_3d(map, ptr, dims, strides, box, CU_TENSOR_MAP_DATA_TYPE_UINT8,
+                 D >= 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
 // 3-D map over a contiguous E4M3 [planes, rows, D] tensor (one byte per
 // element): box = 128 rows x all D bytes (D = 128: one 128-byte swizzle span).
 bool make_tile_map_u8(CUtensorMap* map, const void* ptr, int D, long long rows,
                       long long planes) {
-  const MapKey key{ptr, 3, D, rows, planes, 128u};
-  if (map_cache().find(key, map)) return true;
   const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)rows, (cuuint64_t)planes};
   const cuuint64_t strides[2] = {(cuuint64_t)D, (cuuint64_t)rows * D};
   const cuuint32_t box[3] = {(cuuint32_t)D, 128, 1};
-  if (!encode_3d(map, ptr, dims, strides, box, CU_TENSOR_MAP_DATA_TYPE_UINT8,
-                 CU_TENSOR_MAP_SWIZZLE_128B))
-    return false;
-  map_cache().put(key, *map);
-  return true;
+  return encode_3d(map, ptr, dims, strides, box, CU_TENSOR_MAP_DATA_TYPE_UINT8,
+                 CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
