@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -34,7 +35,7 @@ _I = ctypes.c_int
 _F = ctypes.c_float
 _SZ = ctypes.c_size_t
 _LL = ctypes.c_longlong
-_LL6, _LL12 = _LL * 6, _LL * 12
+_PACK6, _PACK12 = struct.Struct("6q").pack, struct.Struct("12q").pack
 SIGNATURES = {
     "attn_fwd": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F, _P]),
     "attn_fwd_masked": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F, _P, _P]),
@@ -777,6 +778,15 @@ def _new(like, shape, dtype, stream):
         return torch.empty(shape, dtype=dtype, device=like.device)
 
 
+def _new_like(t, stream):
+    """A new contiguous buffer of t's shape and type, as ``_new``."""
+    import torch
+    if stream is None:
+        return torch.empty_like(t, memory_format=torch.contiguous_format)
+    with torch.cuda.stream(stream):
+        return torch.empty_like(t, memory_format=torch.contiguous_format)
+
+
 def _addr(t):
     return None if t is None else t.data_ptr()
 
@@ -818,7 +828,7 @@ def _rope(name, q, k, inv_freq, positions, interleaved, mscale, q_out, k_out, st
     if q.dtype is not bf16 or sq[3] != 1:
         raise ValueError("q must be bfloat16 with contiguous rows")
     if q_out is None:
-        q_out = _new(q, shape, bf16, stream)
+        q_out = _new_like(q, stream)
     elif q_out.shape != shape or q_out.dtype is not bf16 or q_out.stride(3) != 1:
         raise ValueError("q_out must be bfloat16 of q's shape with contiguous rows")
     so = q_out.stride()
@@ -830,7 +840,7 @@ def _rope(name, q, k, inv_freq, positions, interleaved, mscale, q_out, k_out, st
         if kshape != (B, Hkv, S, d) or k.dtype is not bf16 or sk[3] != 1:
             raise ValueError("k must be bfloat16 [B, Hkv, S, d] with contiguous rows")
         if k_out is None:
-            k_out = _new(k, kshape, bf16, stream)
+            k_out = _new_like(k, stream)
         elif k_out.shape != kshape or k_out.dtype is not bf16 or k_out.stride(3) != 1:
             raise ValueError("k_out must be bfloat16 of k's shape with contiguous rows")
         sko = k_out.stride()
@@ -851,7 +861,7 @@ def _rope(name, q, k, inv_freq, positions, interleaved, mscale, q_out, k_out, st
             pos_stride = positions.stride(0)
     _launch(name, index, q.data_ptr(), _addr(k), q_out.data_ptr(), _addr(k_out),
             inv_freq.data_ptr(), _addr(positions), pos_stride, B, Hq, Hkv, S, d, rot,
-            1 if interleaved else 0, float(mscale), _LL12(*strides), raw)
+            1 if interleaved else 0, float(mscale), _PACK12(*strides), raw)
     return q_out, k_out
 
 
@@ -920,7 +930,7 @@ def _append(name, k, v, k_cache, v_cache, k_scale, v_scale, block_table, seq_len
             raise ValueError("q must be bfloat16 [total, Hq, d] with contiguous rows")
         Hq = qshape[1]
         if q_out is None:
-            q_out = _new(q, qshape, bf16, stream)
+            q_out = _new_like(q, stream)
         elif q_out.shape != qshape or q_out.dtype is not bf16 or not q_out.is_contiguous():
             raise ValueError("q_out must be contiguous bfloat16 of q's shape")
         elif q_out.data_ptr() == q.data_ptr() and not q.is_contiguous():
@@ -931,7 +941,7 @@ def _append(name, k, v, k_cache, v_cache, k_scale, v_scale, block_table, seq_len
             v_cache.data_ptr(), *scales, block_table.data_ptr(), _addr(cu_seqlens),
             seq_lens.data_ptr(), _addr(positions), _addr(inv_freq), cache[1], B, Hq, Hkv, total,
             table[1], cache[0], d, rot, 1 if interleaved else 0, float(mscale),
-            _LL6(*sq[:2], *sk[:2], *sv[:2]), raw)
+            _PACK6(*sq[:2], *sk[:2], *sv[:2]), raw)
     return q_out
 
 
@@ -960,6 +970,13 @@ def attn_append_paged_fp8(k, v, k_cache, v_cache, k_scale, v_scale, block_table,
                    q_out, stream)
 
 
+def _buffer_like(t, like, stream, name):
+    """A caller's output buffer of ``like``'s shape and type, checked, or a new one."""
+    if t is None:
+        return _new_like(like, stream)
+    return _buffer(t, like, like.shape, like.dtype, stream, name)
+
+
 def _buffer(t, like, shape, dtype, stream, name):
     """A caller's output buffer, checked, or a new one."""
     if t is None:
@@ -975,6 +992,12 @@ def _workspace(t, like, need, stream):
     if t is None:
         t = _new(like, (max(need, 16),), torch.uint8, stream)
     return t.data_ptr(), t.numel() * t.element_size(), t
+
+
+def _tokens(n):
+    """A token count as a C int: one beyond its range covers every key as well, and one below
+    0 stays refused."""
+    return max(-1, min(int(n), 0x7fffffff))
 
 
 def _dense_shapes(q, k, v, k_lens):
@@ -1001,20 +1024,20 @@ def attn_fwd_window_sinks(q, k, v, scale: float, window: int, sinks: int = 0, k_
     index = _device_index(q, k, v, k_lens, out, lse)
     raw = _raw_stream(stream, index)
     B, Hq, Hkv, Sq, Sk, d = _dense_shapes(q, k, v, k_lens)
-    out = _buffer(out, q, q.shape, torch.bfloat16, stream, "out")
+    out = _buffer_like(out, q, stream, "out")
     if lse is not None or return_lse:
         lse = _buffer(lse, q, (B, Hq, Sq), torch.float32, stream, "lse")
     _launch("attn_fwd_window_sinks", index, q.data_ptr(), k.data_ptr(), v.data_ptr(),
             out.data_ptr(), _addr(lse), B, Hq, Hkv, Sq, Sk, d, float(scale), _addr(k_lens),
-            int(window), int(sinks),
+            _tokens(window), _tokens(sinks),
             raw)
     return out, lse
 
 
 def attn_bwd_window_sinks_workspace_size(B: int, Hq: int, Hkv: int, Sq: int, Sk: int, d: int,
                                          window: int, sinks: int) -> int:
-    return int(load_library().attn_bwd_window_sinks_workspace_size(B, Hq, Hkv, Sq, Sk, d, window,
-                                                                   sinks))
+    return int(load_library().attn_bwd_window_sinks_workspace_size(
+        B, Hq, Hkv, Sq, Sk, d, _tokens(window), _tokens(sinks)))
 
 
 def attn_bwd_window_sinks(q, k, v, o, lse, d_o, scale: float, window: int, sinks: int = 0,
@@ -1031,15 +1054,15 @@ def attn_bwd_window_sinks(q, k, v, o, lse, d_o, scale: float, window: int, sinks
             raise ValueError("o and d_o must be contiguous bfloat16 of q's shape")
     if lse.dtype is not torch.float32 or lse.shape != (B, Hq, Sq) or not lse.is_contiguous():
         raise ValueError("lse must be contiguous float32 [B, Hq, Sq]")
-    dq = _buffer(dq, q, q.shape, bf16, stream, "dq")
-    dk = _buffer(dk, q, k.shape, bf16, stream, "dk")
-    dv = _buffer(dv, q, k.shape, bf16, stream, "dv")
+    dq = _buffer_like(dq, q, stream, "dq")
+    dk = _buffer_like(dk, k, stream, "dk")
+    dv = _buffer_like(dv, v, stream, "dv")
     need = attn_bwd_window_sinks_workspace_size(B, Hq, Hkv, Sq, Sk, d, window, sinks)
     ws, ws_bytes, workspace = _workspace(workspace, q, need, stream)
     _launch("attn_bwd_window_sinks", index, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
             lse.data_ptr(), d_o.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, Hq,
             Hkv, Sq, Sk, d, float(scale), _addr(k_lens),
-            int(window), int(sinks), ws, ws_bytes, raw)
+            _tokens(window), _tokens(sinks), ws, ws_bytes, raw)
     return dq, dk, dv
 
 
@@ -1071,7 +1094,7 @@ def attn_fwd_paged_window(q, k_cache, v_cache, block_table, cu_seqlens_q, seq_le
     _int32(cu_seqlens_q, (B + 1,), "cu_seqlens_q")
     _int32(seq_lens_k, (B,), "seq_lens_k")
     total, Hq, d = qs
-    out = _buffer(out, q, qs, bf16, stream, "out")
+    out = _buffer_like(out, q, stream, "out")
     if lse is not None or return_lse:
         lse = _buffer(lse, q, (Hq, total), torch.float32, stream, "lse")
     need = attn_fwd_paged_window_workspace_size(B, Hq, cache[2], total, max_seqlen_q)
@@ -1079,7 +1102,8 @@ def attn_fwd_paged_window(q, k_cache, v_cache, block_table, cu_seqlens_q, seq_le
     _launch("attn_fwd_paged_window", index, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
             block_table.data_ptr(), cu_seqlens_q.data_ptr(), seq_lens_k.data_ptr(), cache[1], B,
             Hq, cache[2], total, max_seqlen_q, table[1], cache[0], d,
-            float(scale), int(window), int(sinks), out.data_ptr(), _addr(lse), ws, ws_bytes, raw)
+            float(scale), _tokens(window), _tokens(sinks), out.data_ptr(), _addr(lse), ws, ws_bytes,
+            raw)
     return out, lse
 
 
@@ -1111,12 +1135,13 @@ def _decode_window(name, q, k_cache, v_cache, k_scale, v_scale, block_table, seq
             or not block_table.is_contiguous():
         raise ValueError("block_table must be contiguous int32 [B, max_pages_per_seq]")
     _int32(seq_lens, (B,), "seq_lens")
-    out = _buffer(out, q, qs, bf16, stream, "out")
+    out = _buffer_like(out, q, stream, "out")
     if lse is not None or return_lse:
         lse = _buffer(lse, q, (B, Hq), torch.float32, stream, "lse")
     _launch(name, index, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), *scales,
             block_table.data_ptr(), seq_lens.data_ptr(), cache[1], B, Hq, cache[2], d, table[1],
-            cache[0], float(scale), int(window), int(sinks), out.data_ptr(), _addr(lse), raw)
+            cache[0], float(scale), _tokens(window), _tokens(sinks), out.data_ptr(), _addr(lse),
+            raw)
     return out, lse
 
 

@@ -567,7 +567,8 @@ int attn_bwd_varlen(const void* q, const void* k, const void* v, const void* o, 
  *   k_out NULL): queries only.
  *   inv_freq  [rotary_dim / 2] float64 device array: radians per position of
  *             each pair, whatever scheme made them (bases, stretched or ramped
- *             frequencies for long contexts); 8-byte aligned.
+ *             frequencies for long contexts); finite, below 2^20 in magnitude;
+ *             8-byte aligned.
  *   positions int32 device array, any values: row s of sequence b is at
  *             positions[b * pos_stride + s] (pos_stride 0: shared by the
  *             batch); NULL: s.

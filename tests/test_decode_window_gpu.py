@@ -59,6 +59,7 @@ CASES = [
     ([900, 20], 4, 2, 64, 16, 17, 2000),               # all keys are first tokens
     ([900, 20], 4, 2, 64, 16, 5000, 4),                # the window is every key
     ([900, 0], 4, 2, 128, 16, 0, 4),                   # no window
+    ([900, 33], 4, 2, 64, 16, 2 ** 40, 2 ** 35),       # counts beyond an int
     ([5000], 2, 1, 64, 16, 4500, 4),                   # more chunks than one round of the warps holds
     ([2100] * 40, 8, 8, 64, 16, 2000, 5),              # several rounds in a cluster of one
 ]

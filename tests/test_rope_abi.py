@@ -134,3 +134,9 @@ def test_binding_refuses_host_tensors():
     with pytest.raises(ValueError, match="CUDA"):
         B.attn_append_paged(k, k, c, c, torch.zeros(2, 2, dtype=torch.int32),
                             torch.ones(2, dtype=torch.int32))
+
+
+def test_counts_are_clamped_to_a_c_int():
+    assert B._tokens(5) == 5 and B._tokens(2 ** 31 - 1) == 2 ** 31 - 1
+    assert B._tokens(2 ** 31) == 2 ** 31 - 1 and B._tokens(2 ** 40 + 7) == 2 ** 31 - 1
+    assert B._tokens(-3) == -1 and B._tokens(-2 ** 40) == -1

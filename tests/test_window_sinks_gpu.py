@@ -129,6 +129,24 @@ def test_without_first_tokens_the_bits_are_the_window_calls():
     assert torch.equal(oc, o3) and torch.equal(lc, l3)
 
 
+def test_no_keys_and_counts_beyond_an_int():
+    q = W.randn_bf16((2, 4, 70, 64), 202).to(DEV)
+    none = torch.empty(2, 2, 0, 64, dtype=torch.bfloat16, device=DEV)
+    o, lse = attn_fwd_window_sinks(q, none, none, 0.1, 8, 2)
+    assert bool((o == 0).all()) and bool(torch.isneginf(lse).all())
+    dq, dk, dv = attn_bwd_window_sinks(q, none, none, o, lse, q, 0.1, 8, 2)
+    assert bool((dq == 0).all()) and dk.shape == none.shape == dv.shape
+    _, k, v = _dev(*W.prefill_inputs(2, 4, 2, 70, 300, 64, 203))
+    for far, near in (((2 ** 40 + 3, 2 ** 33), (300, 0)), ((8, 2 ** 32 + 1), (8, 300))):
+        a = attn_fwd_window_sinks(q, k, v, 0.1, *far)
+        b = attn_fwd_window_sinks(q, k, v, 0.1, *near)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+        for x, y in zip(attn_bwd_window_sinks(q, k, v, *a, q, 0.1, *far),
+                        attn_bwd_window_sinks(q, k, v, *b, q, 0.1, *near)):
+            assert torch.equal(x, y)
+    _ok()
+
+
 @pytest.mark.parametrize("scale", [-0.2, 0.0, 3.0])
 def test_odd_scales(scale):
     q, k, v = W.prefill_inputs(1, 2, 1, 400, 400, 64, 194)
@@ -156,6 +174,7 @@ PAGED = [
     ([1, 9, 140], [40, 700, 300], 16, 1, 64, 64, 50, 33),  # 16
     ([31, 65], [400, 65], 12, 2, 128, 32, 64, 4),          # 6: tiles of one head
     ([5, 9], [3, 9], 2, 1, 64, 16, 4, 2),                  # more queries than keys: empty rows
+    ([4, 2, 140], [0, 2, 1], 8, 2, 128, 16, 4, 2),         # no keys, one key
 ]
 
 
