@@ -194,17 +194,21 @@ struct BwdCfg {
   static constexpr int Q_OFF_K = 2 * TILE_BYTES;
   static constexpr int Q_OFF_V = Q_OFF_K + STAGES * TILE_BYTES;
   static constexpr int Q_OFF_BAR = Q_OFF_V + STAGES * TILE_BYTES;
-  static constexpr int QB_QF = 0;                  // Q and dO landed
+  static constexpr int QB_QF = 0;                  // Q and dO of a unit landed
   static constexpr int QB_KVF = 1;                 // STAGES: K and V landed
   static constexpr int QB_KVE = QB_KVF + STAGES;   // STAGES: stage free
   static constexpr int QB_SF = QB_KVE + STAGES;    // 2: S in TMEM buffer 0 / 1
   static constexpr int QB_DPF = QB_SF + 2;         // dP in TMEM
   static constexpr int QB_DSF = QB_DPF + 1;        // dS written (256 threads)
-  static constexpr int QB_ACC = QB_DSF + 1;
-  static constexpr int QB_NUM = QB_ACC + 1;
-  static constexpr int Q_OFF_MISC = Q_OFF_BAR + QB_NUM * 8;
-  static constexpr int Q_SMEM = Q_OFF_MISC + 16 + 1024;
-  static constexpr int Q_OFF_LIST = Q_OFF_MISC + 16;
+  static constexpr int QB_ACC = QB_DSF + 1;        // every MMA of a unit retired
+  static constexpr int QB_QE = QB_ACC + 1;         // the last MMA that reads Q and dO retired
+  static constexpr int QB_NF = QB_QE + 1;          // 2: next unit's id arrived
+  static constexpr int QB_NE = QB_NF + 2;          // 2: and was read by all (MMA + 8 warps)
+  static constexpr int QB_NUM = QB_NE + 2;
+  static constexpr int Q_OFF_MISC = Q_OFF_BAR + QB_NUM * 8;  // tmem base, abort flag, list count
+  static constexpr int Q_OFF_NEXT = (Q_OFF_MISC + 12 + 15) / 16 * 16;  // 2 answers of 16 bytes
+  static constexpr int Q_SMEM = Q_OFF_NEXT + 32 + 1024;
+  static constexpr int Q_OFF_LIST = Q_OFF_NEXT + 32;
   static constexpr int Q_SMEM_MASKS = Q_SMEM + 3 * LIST_MAX;
   // ---- tensor memory (512 columns)
   static constexpr uint32_t TMEM_COLS = 512;
@@ -707,10 +711,87 @@ __global__ void __launch_bounds__(256) attn_bwd_far_join_kernel(const BwdParams 
 }
 
 // ===========================================================================
-// dQ: one CTA per (query tile, batch, query head).  Units are numbered query
-// tile major from the last tile down, so under a causal mask the heaviest
-// tiles start first.
+// dQ: one unit per (query tile, batch, query head), numbered query tile major
+// from the last tile down, so under a causal mask the heaviest tiles start
+// first.  The grid has a CTA per unit, but a CTA that runs goes on with the
+// units of CTAs that have not started yet: it cancels their launch
+// (clusterlaunchcontrol.try_cancel) and takes over their index.  Units are thus
+// still dealt as SMs become free, also beside the tail of the dK/dV grid, and
+// a CTA loads the next unit's first K, V, Q and dO while it finishes the
+// current one; as launches of their own the units paid about 6 us each for
+// start, first loads and end (of 21 us at a window of 1024 and d = 128).  With a
+// block mask, whose list of key tiles is made by the whole CTA, it computes its
+// own unit alone.
 // ===========================================================================
+struct BwdQUnit {
+  BwdSeq sq;
+  int b, hq, kvh, bh_q, bh_kv, qt, row0, klen, n_rows;
+  long long koff;
+  int kt_lo, st, n;  // key tiles walked: [0, st) (first tokens), then from kt_lo on; n in all
+};
+
+template <bool CAUSAL, bool VARLEN, bool MASKS>
+__device__ __forceinline__ void bwd_q_unit(const BwdParams& p, int id, bool report, BwdQUnit& u) {
+  u.bh_q = id % (p.B * p.Hq);
+  u.qt = p.n_qt - 1 - id / (p.B * p.Hq);
+  u.b = u.bh_q / p.Hq;
+  u.hq = u.bh_q % p.Hq;
+  u.kvh = u.hq / p.group;
+  u.bh_kv = u.b * p.Hkv + u.kvh;
+  const bool seq_ok = bwd_sequence<VARLEN>(p, u.b, report, u.sq);
+  u.klen = seq_ok ? u.sq.lk : 0;
+  u.n_rows = seq_ok ? u.sq.lq : 0;  // dQ rows of this sequence
+  u.koff = (long long)u.klen - u.sq.lq;
+  u.row0 = u.qt * 128;
+  const int last_row = min(u.row0 + 127, u.n_rows - 1);
+  long long max_key = (long long)u.klen - 1;  // the last key any row of the tile sees
+  if (CAUSAL)
+    max_key =
+        min(max_key, max((long long)last_row + u.koff, MASKS ? (long long)p.prefix - 1 : -1LL));
+  // the first key tile any row sees (a sliding window starts it past 0)
+  u.kt_lo = 0;
+  if (MASKS && p.window > 0) {
+    const long long min_key = (long long)u.row0 + u.koff - p.window + 1;
+    u.kt_lo = min_key <= 0 ? 0 : (int)(min_key / 128);
+  }
+  // none for a tile past the sequence's rows
+  const int kt_end = max_key < 0 ? 0 : (int)(max_key / 128) + 1;
+  // the tiles of visible first tokens, when the window leaves a gap behind them
+  u.st = 0;
+  if (MASKS && p.sinks > 0) {
+    u.st = (min(p.sinks, u.klen) + 127) / 128;
+    if (u.kt_lo <= u.st) u.kt_lo = u.st = 0;
+  }
+  u.n = (u.row0 >= u.n_rows || kt_end <= u.kt_lo) ? 0 : u.st + kt_end - u.kt_lo;
+}
+
+// Asks for the index of a CTA of this grid that has not started; the 16-byte
+// answer arrives at `dst` (shared memory) and counts on `bar`.
+__device__ __forceinline__ void bwd_ask_next(uint32_t dst, uint32_t bar) {
+  fence_proxy_async_smem();  // the reads of the slot's last answer precede this one
+  mbar_arrive_expect_tx(bar, 16);
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], "
+      "[%1];" ::"r"(dst),
+      "r"(bar)
+      : "memory");
+}
+
+// The answer: a CTA index (x), or -1 when no CTA was left to take over.
+__device__ __forceinline__ int bwd_read_next(uint32_t src) {
+  int id;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\t"
+      "ld.shared.b128 r, [%1];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+      "mov.b32 %0, -1;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, r;\n\t}"
+      : "=r"(id)
+      : "r"(src)
+      : "memory");
+  return id;
+}
+
 template <int D, bool CAUSAL, bool VARLEN, bool MASKS>
 __global__ void __launch_bounds__(384, 1)
     attn_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q,
@@ -728,45 +809,22 @@ __global__ void __launch_bounds__(384, 1)
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
 
-  const int bh_q = blockIdx.x % (p.B * p.Hq);
-  const int qt = p.n_qt - 1 - (int)(blockIdx.x / (p.B * p.Hq));
-  const int b = bh_q / p.Hq, hq = bh_q % p.Hq;
-  const int kvh = hq / p.group;
-  const int bh_kv = b * p.Hkv + kvh;
-  BwdSeq sq;
-  const bool seq_ok = bwd_sequence<VARLEN>(p, b, threadIdx.x == 0, sq);
-  const int klen = seq_ok ? sq.lk : 0;
-  const int n_rows = seq_ok ? sq.lq : 0;  // dQ rows of this sequence
-  const long long koff = (long long)klen - sq.lq;
-  const int row0 = qt * 128;
-  const int last_row = min(row0 + 127, n_rows - 1);
-  long long max_key = (long long)klen - 1;  // the last key any row of the tile sees
-  if (CAUSAL)
-    max_key = min(max_key, max((long long)last_row + koff, MASKS ? (long long)p.prefix - 1 : -1LL));
-  // the first key tile any row sees (a sliding window starts it past 0)
-  int kt_lo = 0;
-  if (MASKS && p.window > 0) {
-    const long long min_key = (long long)row0 + koff - p.window + 1;
-    kt_lo = min_key <= 0 ? 0 : (int)(min_key / 128);
-  }
-  // key tiles [kt_lo, kt_lo + N); none for a tile past the sequence's rows
-  const int kt_end = max_key < 0 ? 0 : (int)(max_key / 128) + 1;
-  // the tiles of visible first tokens, when the window leaves a gap behind them
-  int st = 0;
-  if (MASKS && p.sinks > 0) {
-    st = (min(p.sinks, klen) + 127) / 128;
-    if (kt_lo <= st) kt_lo = st = 0;
-  }
-  const int N = (row0 >= n_rows || kt_end <= kt_lo) ? 0 : st + kt_end - kt_lo;
-  // with a block mask, only the key tiles whose block is on are walked
-  const bool listed = MASKS && p.block_mask != nullptr && N > 0 && N <= C::LIST_MAX;
+  // with a block mask, only the key tiles whose block is on are walked, and the
+  // CTA takes no unit but its own
+  const bool masked = MASKS && p.block_mask != nullptr;
   const uint16_t* list = reinterpret_cast<const uint16_t*>(sbase_ptr + C::Q_OFF_LIST);
   int* list_count = reinterpret_cast<int*>(sbase_ptr + C::Q_OFF_MISC + 8);
-  if (listed)
-    bwd_list_blocks(
-        N, [&](int c) { return bwd_block_on(p, b, hq, qt, kt_lo + c); },
-        reinterpret_cast<uint16_t*>(sbase_ptr + C::Q_OFF_LIST),
-        sbase_ptr + C::Q_OFF_LIST + 2 * C::LIST_MAX, list_count);
+  bool listed = false;
+  if (masked) {
+    BwdQUnit u;
+    bwd_q_unit<CAUSAL, VARLEN, MASKS>(p, blockIdx.x, false, u);
+    listed = u.n > 0 && u.n <= C::LIST_MAX;
+    if (listed)
+      bwd_list_blocks(
+          u.n, [&](int c) { return bwd_block_on(p, u.b, u.hq, u.qt, u.kt_lo + c); },
+          reinterpret_cast<uint16_t*>(sbase_ptr + C::Q_OFF_LIST),
+          sbase_ptr + C::Q_OFF_LIST + 2 * C::LIST_MAX, list_count);
+  }
 
   if (threadIdx.x == 0) {
     mbar_init(bar(C::QB_QF), 1);
@@ -774,11 +832,15 @@ __global__ void __launch_bounds__(384, 1)
       mbar_init(bar(C::QB_KVF + s), 1);
       mbar_init(bar(C::QB_KVE + s), 1);
     }
-    mbar_init(bar(C::QB_SF), 1);
-    mbar_init(bar(C::QB_SF + 1), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(C::QB_SF + i), 1);
+      mbar_init(bar(C::QB_NF + i), 1);
+      mbar_init(bar(C::QB_NE + i), 1 + 8);
+    }
     mbar_init(bar(C::QB_DPF), 1);
     mbar_init(bar(C::QB_DSF), 256);
     mbar_init(bar(C::QB_ACC), 1);
+    mbar_init(bar(C::QB_QE), 1);
     *abort_flag = 0;
     mbar_init_fence();
     fence_proxy_async_smem();
@@ -791,10 +853,21 @@ __global__ void __launch_bounds__(384, 1)
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
-  const int NI = listed ? *list_count : N;  // key tiles walked
-  // the n-th key tile walked
-  auto key_tile = [&](int n) {
-    return listed ? kt_lo + (int)list[n] : (MASKS && n < st) ? n : kt_lo + n - (MASKS ? st : 0);
+  // the n-th key tile of a unit, and how many it walks
+  auto key_tile = [&](const BwdQUnit& u, int n) {
+    return listed ? u.kt_lo + (int)list[n]
+                  : (MASKS && n < u.st) ? n : u.kt_lo + n - (MASKS ? u.st : 0);
+  };
+  auto n_tiles = [&](const BwdQUnit& u) { return listed ? *list_count : u.n; };
+  // Unit k > 0's id: slot k & 1, its ((k - 1) >> 1)-th use.  Waits for the
+  // answer, reads it and frees the slot; -1 when there is none (or on an abort).
+  auto slot = [&](int k) { return sbase + C::Q_OFF_NEXT + 16u * (uint32_t)(k & 1); };
+  auto next_unit = [&](int k, bool frees) -> int {
+    if (masked) return -1;
+    if (!mbar_wait(bar(C::QB_NF + (k & 1)), ((k - 1) >> 1) & 1u, abort_flag)) return -1;
+    const int id = bwd_read_next(slot(k));
+    if (frees) mbar_arrive(bar(C::QB_NE + (k & 1)));
+    return id;
   };
   const uint32_t sQ = sbase + C::Q_OFF_Q, sDO = sbase + C::Q_OFF_DO;
   auto sK = [&](int s) { return sbase + C::Q_OFF_K + (uint32_t)s * C::TILE_BYTES; };
@@ -802,69 +875,138 @@ __global__ void __launch_bounds__(384, 1)
 
   if (warp < 4) {
     warpgroup_reg_dealloc<C::REGS_PRODUCER>();
-    if (warp == 0 && lane == 0 && NI > 0) {
+    if (warp == 0 && lane == 0) {
       // ======================= TMA producer =======================
       tma_prefetch_map(&tm_q);
       tma_prefetch_map(&tm_do);
       tma_prefetch_map(&tm_k);
       tma_prefetch_map(&tm_v);
-      mbar_arrive_expect_tx(bar(C::QB_QF), 2 * C::TILE_BYTES);
-      const int qy = VARLEN ? hq : row0, qz = VARLEN ? sq.q0 + row0 : bh_q;
-      for (int cb = 0; cb < C::NCB; ++cb) {
-        tma_load_3d(sQ + cb * C::CB_BYTES, &tm_q, bar(C::QB_QF), 64 * cb, qy, qz);
-        tma_load_3d(sDO + cb * C::CB_BYTES, &tm_do, bar(C::QB_QF), 64 * cb, qy, qz);
-      }
-      int issued = 0;
+      int q_loads = 0, kv = 0;  // Q and dO, and K and V tiles, issued so far
+      int asked = 0;            // requests for a next unit issued so far
       bool ok = true;
-      for (int n = 0; n < NI; ++n) {
-        const int s = n % C::STAGES;
-        if (n >= C::STAGES &&
-            !(ok = mbar_wait(bar(C::QB_KVE + s), ((n / C::STAGES) - 1) & 1u, abort_flag)))
-          break;
-        mbar_arrive_expect_tx(bar(C::QB_KVF + s), 2 * C::TILE_BYTES);
-        const int kt = key_tile(n);
-        const int ky = VARLEN ? kvh : kt * 128, kz = VARLEN ? sq.k0 + kt * 128 : bh_kv;
+      auto load_q = [&](const BwdQUnit& u) -> bool {
+        if (q_loads > 0 && !mbar_wait(bar(C::QB_QE), (q_loads - 1) & 1u, abort_flag)) return false;
+        mbar_arrive_expect_tx(bar(C::QB_QF), 2 * C::TILE_BYTES);
+        const int qy = VARLEN ? u.hq : u.row0, qz = VARLEN ? u.sq.q0 + u.row0 : u.bh_q;
         for (int cb = 0; cb < C::NCB; ++cb) {
-          tma_load_3d(sK(s) + cb * C::CB_BYTES, &tm_k, bar(C::QB_KVF + s), 64 * cb, ky, kz);
-          tma_load_3d(sV(s) + cb * C::CB_BYTES, &tm_v, bar(C::QB_KVF + s), 64 * cb, ky, kz);
+          tma_load_3d(sQ + cb * C::CB_BYTES, &tm_q, bar(C::QB_QF), 64 * cb, qy, qz);
+          tma_load_3d(sDO + cb * C::CB_BYTES, &tm_do, bar(C::QB_QF), 64 * cb, qy, qz);
         }
-        ++issued;
+        ++q_loads;
+        return true;
+      };
+      int id = blockIdx.x;
+      for (int k = 0; ok && id >= 0; ++k) {
+        if (!masked) {  // the next unit, while this one is loaded and computed
+          if (k >= 2 && !(ok = mbar_wait(bar(C::QB_NE + ((k + 1) & 1)), ((k - 2) >> 1) & 1u,
+                                         abort_flag)))
+            break;
+          bwd_ask_next(slot(k + 1), bar(C::QB_NF + ((k + 1) & 1)));
+          ++asked;
+        }
+        BwdQUnit u;
+        bwd_q_unit<CAUSAL, VARLEN, MASKS>(p, id, true, u);
+        const int NI = n_tiles(u);
+        for (int n = 0; n < NI; ++n) {
+          const int s = kv % C::STAGES;
+          if (kv >= C::STAGES &&
+              !(ok = mbar_wait(bar(C::QB_KVE + s), ((kv / C::STAGES) - 1) & 1u, abort_flag)))
+            break;
+          mbar_arrive_expect_tx(bar(C::QB_KVF + s), 2 * C::TILE_BYTES);
+          const int kt = key_tile(u, n);
+          const int ky = VARLEN ? u.kvh : kt * 128, kz = VARLEN ? u.sq.k0 + kt * 128 : u.bh_kv;
+          for (int cb = 0; cb < C::NCB; ++cb) {
+            tma_load_3d(sK(s) + cb * C::CB_BYTES, &tm_k, bar(C::QB_KVF + s), 64 * cb, ky, kz);
+            tma_load_3d(sV(s) + cb * C::CB_BYTES, &tm_v, bar(C::QB_KVF + s), 64 * cb, ky, kz);
+          }
+          ++kv;
+          // Q and dO behind the first K and V: their buffers free later
+          if (n == 0 && !(ok = load_q(u))) break;
+        }
+        if (!ok) break;
+        id = next_unit(k + 1, false);
       }
-      mbar_wait(bar(C::QB_QF), 0, nullptr);
-      for (int n = (issued > C::STAGES ? issued - C::STAGES : 0); n < issued; ++n)
+      // Drain: no copy and no answer may still be on its way when the CTA exits.
+      if (q_loads > 0) mbar_wait(bar(C::QB_QF), (q_loads - 1) & 1u, nullptr);
+      for (int n = (kv > C::STAGES ? kv - C::STAGES : 0); n < kv; ++n)
         mbar_wait(bar(C::QB_KVF + n % C::STAGES), (n / C::STAGES) & 1u, nullptr);
-    } else if (warp == 1 && lane == 0 && NI > 0) {
+      if (asked > 0)
+        mbar_wait(bar(C::QB_NF + (asked & 1)), ((asked - 1) >> 1) & 1u, nullptr);
+    } else if (warp == 1) {
       // ======================= tcgen05 MMA issuer =======================
+      // The whole warp walks the schedule and one elected lane issues, as in the
+      // forward.  `it` counts key tiles over all units: ring stage, S buffer and
+      // phases.
       const uint32_t tDP = tmem + C::Q_TM_DP, tDQ = tmem + C::Q_TM_DQ;
       auto tS = [&](int n) { return tmem + ((n & 1) ? C::Q_TM_S1 : C::Q_TM_S0); };
-      bool ok = mbar_wait(bar(C::QB_QF), 0, abort_flag) && mbar_wait(bar(C::QB_KVF), 0, abort_flag);
-      if (ok) {
-        tc_fence_after_sync();
-        bwd_mma_ss<D>(tS(0), sQ, sK(0));
-        umma_commit(bar(C::QB_SF));
-        bwd_mma_ss<D>(tDP, sDO, sV(0));
-        umma_commit(bar(C::QB_DPF));
-      }
-      for (int n = 0; ok && n < NI; ++n) {
-        const int s = n % C::STAGES, s1 = (n + 1) % C::STAGES;
-        if (n + 1 < NI) {
-          if (!(ok = mbar_wait(bar(C::QB_KVF + s1), ((n + 1) / C::STAGES) & 1u, abort_flag))) break;
+      auto wait = [&](uint32_t b, uint32_t ph) -> bool {
+        if (__all_sync(0xffffffffu, mbar_test(b, ph))) return true;
+        const bool r = mbar_wait_slow(b, ph, abort_flag);
+        return __all_sync(0xffffffffu, r);
+      };
+      int it = 0, units = 0;
+      bool ok = true;
+      int id = blockIdx.x;
+      for (int k = 0; ok && id >= 0; ++k) {
+        BwdQUnit u;
+        bwd_q_unit<CAUSAL, VARLEN, MASKS>(p, id, false, u);
+        const int NI = n_tiles(u);
+        if (NI > 0) {
+          const int s0 = it % C::STAGES;
+          // S and dP of the first tile.  Their buffers were read before dS of the
+          // unit before, which has been waited for.
+          if (!(ok = wait(bar(C::QB_QF), units & 1u) &&
+                     wait(bar(C::QB_KVF + s0), (it / C::STAGES) & 1u)))
+            break;
           tc_fence_after_sync();
-          bwd_mma_ss<D>(tS(n + 1), sQ, sK(s1));
-          umma_commit(bar(C::QB_SF + ((n + 1) & 1)));
+          if (elect_one()) {
+            bwd_mma_ss<D>(tS(it), sQ, sK(s0));
+            umma_commit(bar(C::QB_SF + (it & 1)));
+            bwd_mma_ss<D>(tDP, sDO, sV(s0));
+            umma_commit(bar(C::QB_DPF));
+            if (NI == 1) umma_commit(bar(C::QB_QE));
+          }
+          __syncwarp();
+          for (int n = 0; n < NI; ++n, ++it) {
+            const int s = it % C::STAGES, s1 = (it + 1) % C::STAGES;
+            if (n + 1 < NI) {
+              if (!(ok = wait(bar(C::QB_KVF + s1), ((it + 1) / C::STAGES) & 1u))) break;
+              tc_fence_after_sync();
+              if (elect_one()) {
+                bwd_mma_ss<D>(tS(it + 1), sQ, sK(s1));
+                umma_commit(bar(C::QB_SF + ((it + 1) & 1)));
+              }
+              __syncwarp();
+            }
+            if (!(ok = wait(bar(C::QB_DSF), it & 1u))) break;
+            tc_fence_after_sync();
+            if (elect_one()) {
+              // dQ += dS K.  A unit's first one overwrites the last unit's dQ, which
+              // was stored before its threads wrote this dS.
+              bwd_mma_ts<D>(tDQ, tDP, sK(s), n > 0);
+              umma_commit(bar(C::QB_KVE + s));
+              if (n + 1 < NI) {
+                // dP of the next key tile: overwrites dS only after the MMA above read it
+                bwd_mma_ss<D>(tDP, sDO, sV(s1));
+                umma_commit(bar(C::QB_DPF));
+                if (n + 2 == NI) umma_commit(bar(C::QB_QE));
+              } else {
+                umma_commit(bar(C::QB_ACC));
+              }
+            }
+            __syncwarp();
+          }
+          if (!ok) break;
+          ++units;
         }
-        if (!(ok = mbar_wait(bar(C::QB_DSF), n & 1u, abort_flag))) break;
-        tc_fence_after_sync();
-        bwd_mma_ts<D>(tDQ, tDP, sK(s), n > 0);  // dQ += dS K
-        umma_commit(bar(C::QB_KVE + s));
-        if (n + 1 < NI) {
-          // dP of the next key tile: overwrites dS only after the MMA above read it
-          bwd_mma_ss<D>(tDP, sDO, sV(s1));
-          umma_commit(bar(C::QB_DPF));
-        }
+        if (lane == 0) id = next_unit(k + 1, true);
+        id = __shfl_sync(0xffffffffu, id, 0);
       }
-      umma_commit(bar(C::QB_ACC));
-      mbar_wait(bar(C::QB_ACC), 0, nullptr);
+      // every MMA issued above retires before TMEM is freed; an aborted unit's by a commit of
+      // its own
+      if (!ok && elect_one()) umma_commit(bar(C::QB_ACC));
+      __syncwarp();
+      if (units > 0 || !ok) mbar_wait(bar(C::QB_ACC), (ok ? units - 1 : units) & 1u, nullptr);
     }
     __syncwarp();
   } else {
@@ -876,107 +1018,136 @@ __global__ void __launch_bounds__(384, 1)
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
     const int c0 = 64 * wg;
     const uint32_t t_dp = tmem + lane_off + C::Q_TM_DP + c0;
-    const int row = row0 + r;
-    const size_t srow = (size_t)bh_q * p.Sq_pad + row;
-    const float nl = p.nlse2[srow];
-    const float dd = p.dsum[srow];
     const uint64_t c2x2 = f32x2(p.scale_log2, p.scale_log2);
-    const uint64_t nlx2 = f32x2(nl, nl);
-    // keys klo <= j < kend are visible to this row
-    long long kend = klen, klo = 0;
-    if (CAUSAL)
-      kend = min(kend, max((long long)row + koff, MASKS ? (long long)p.prefix - 1 : -1LL) + 1);
-    if (MASKS && p.window > 0) klo = max(0LL, (long long)row + koff - p.window + 1);
+    int it = 0, units = 0;
     bool ok = true;
-    for (int n = 0; ok && n < NI; ++n) {
-      const int kt = key_tile(n);
-      const long long t0 = (long long)kt * 128 + c0;  // this run's first key
-      long long cm = kend - t0;  // visible iff cmin <= c < cmax
-      if (MASKS && !bwd_block_on(p, b, hq, qt, kt)) cm = 0;
-      const long long cn = MASKS ? klo - t0 : 0;
-      const int cmin = (int)(cn < 0 ? 0 : (cn > 64 ? 64 : cn));
-      const int cmax = (int)(cm < 0 ? 0 : (cm > 64 ? 64 : cm));
-      // columns below csink are first tokens, visible below cmin too
-      const long long cs = MASKS ? (long long)p.sinks - t0 : 0;
-      const int csink = MASKS ? (int)(cs < 0 ? 0 : (cs > 64 ? 64 : cs)) : 0;
-      const bool edge = __any_sync(0xffffffffu, cmax < 64 || cmin > 0);
-      uint32_t vis[2];  // the visible columns as words of bits (masked kernels)
+    int id = blockIdx.x;
+    BwdQUnit u;
+    bwd_q_unit<CAUSAL, VARLEN, MASKS>(p, id, false, u);
+    auto stat = [&](const float* x, const BwdQUnit& v) {
+      return x[(size_t)v.bh_q * p.Sq_pad + v.row0 + r];
+    };
+    float nl = stat(p.nlse2, u), dd = stat(p.dsum, u);
+    for (int k = 0; id >= 0; ++k) {
+      const int NI = n_tiles(u);
+      const int row = u.row0 + r;
+      const uint64_t nlx2 = f32x2(nl, nl);
+      // keys klo <= j < kend are visible to this row
+      long long kend = u.klen, klo = 0;
+      if (CAUSAL)
+        kend = min(kend, max((long long)row + u.koff, MASKS ? (long long)p.prefix - 1 : -1LL) + 1);
+      if (MASKS && p.window > 0) klo = max(0LL, (long long)row + u.koff - p.window + 1);
+      for (int n = 0; n < NI; ++n, ++it) {
+        const int kt = key_tile(u, n);
+        const long long t0 = (long long)kt * 128 + c0;  // this run's first key
+        long long cm = kend - t0;  // visible iff cmin <= c < cmax
+        if (MASKS && !bwd_block_on(p, u.b, u.hq, u.qt, kt)) cm = 0;
+        const long long cn = MASKS ? klo - t0 : 0;
+        const int cmin = (int)(cn < 0 ? 0 : (cn > 64 ? 64 : cn));
+        const int cmax = (int)(cm < 0 ? 0 : (cm > 64 ? 64 : cm));
+        // columns below csink are first tokens, visible below cmin too
+        const long long cs = MASKS ? (long long)p.sinks - t0 : 0;
+        const int csink = MASKS ? (int)(cs < 0 ? 0 : (cs > 64 ? 64 : cs)) : 0;
+        const bool edge = __any_sync(0xffffffffu, cmax < 64 || cmin > 0);
+        uint32_t vis[2];  // the visible columns as words of bits (masked kernels)
 #pragma unroll
-      for (int w = 0; w < 2; ++w)
-        vis[w] = low_bits(cmax - 32 * w) & (~low_bits(cmin - 32 * w) | low_bits(csink - 32 * w));
-      if (!(ok = mbar_wait_warp(bar(C::QB_SF + (n & 1)), (n >> 1) & 1u, abort_flag))) break;
-      tc_fence_after_sync();
-      const uint32_t t_s = tmem + lane_off + ((n & 1) ? C::Q_TM_S1 : C::Q_TM_S0) + c0;
-      float pr[64];
-      {
-        uint32_t a[32], bq[32];
-        tmem_ld32(t_s, a);
-        tmem_ld32(t_s + 32, bq);
-        tmem_ld_wait();
-        reg_fence32(a);
-        reg_fence32(bq);
+        for (int w = 0; w < 2; ++w)
+          vis[w] = low_bits(cmax - 32 * w) & (~low_bits(cmin - 32 * w) | low_bits(csink - 32 * w));
+        if (!(ok = mbar_wait_warp(bar(C::QB_SF + (it & 1)), (it >> 1) & 1u, abort_flag))) break;
+        tc_fence_after_sync();
+        const uint32_t t_s = tmem + lane_off + ((it & 1) ? C::Q_TM_S1 : C::Q_TM_S0) + c0;
+        float pr[64];
+        {
+          uint32_t a[32], bq[32];
+          tmem_ld32(t_s, a);
+          tmem_ld32(t_s + 32, bq);
+          tmem_ld_wait();
+          reg_fence32(a);
+          reg_fence32(bq);
 #pragma unroll
-        for (int c = 0; c < 64; c += 2) {
-          const uint32_t s0 = c < 32 ? a[c] : bq[c - 32];
-          const uint32_t s1 = c < 32 ? a[c + 1] : bq[c - 31];
-          float x0, x1;
-          split_f32x2(fma_f32x2(f32x2(__uint_as_float(s0), __uint_as_float(s1)), c2x2, nlx2), x0,
-                      x1);
-          if (edge) {
-            x0 = bwd_keep(MASKS ? (vis[c >> 5] & (1u << (c & 31))) != 0 : c < cmax, x0);
-            x1 = bwd_keep(MASKS ? (vis[c >> 5] & (2u << (c & 31))) != 0 : c + 1 < cmax, x1);
+          for (int c = 0; c < 64; c += 2) {
+            const uint32_t s0 = c < 32 ? a[c] : bq[c - 32];
+            const uint32_t s1 = c < 32 ? a[c + 1] : bq[c - 31];
+            float x0, x1;
+            split_f32x2(fma_f32x2(f32x2(__uint_as_float(s0), __uint_as_float(s1)), c2x2, nlx2), x0,
+                        x1);
+            if (edge) {
+              x0 = bwd_keep(MASKS ? (vis[c >> 5] & (1u << (c & 31))) != 0 : c < cmax, x0);
+              x1 = bwd_keep(MASKS ? (vis[c >> 5] & (2u << (c & 31))) != 0 : c + 1 < cmax, x1);
+            }
+            pr[c] = ex2(x0);
+            pr[c + 1] = ex2(x1);
           }
-          pr[c] = ex2(x0);
-          pr[c + 1] = ex2(x1);
+        }
+        if (!(ok = mbar_wait_warp(bar(C::QB_DPF), it & 1u, abort_flag))) break;
+        tc_fence_after_sync();
+        {
+          uint32_t a[32], bq[32];
+          tmem_ld32(t_dp, a);
+          tmem_ld32(t_dp + 32, bq);
+          tmem_ld_wait();
+          reg_fence32(a);
+          reg_fence32(bq);
+          uint32_t pk[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const int c = 2 * e;
+            const float d0 = __uint_as_float(c < 32 ? a[c] : bq[c - 32]) - dd;
+            const float d1 = __uint_as_float(c < 32 ? a[c + 1] : bq[c - 31]) - dd;
+            pk[e] = pack_bf16x2(pr[c] * d0, pr[c + 1] * d1);
+          }
+          tmem_st32(t_dp, pk);  // dS into the first 32 columns of this warpgroup's run
+          tmem_st_wait();
+          tc_fence_before_sync();
+          mbar_arrive(bar(C::QB_DSF));
         }
       }
-      if (!(ok = mbar_wait_warp(bar(C::QB_DPF), n & 1u, abort_flag))) break;
-      tc_fence_after_sync();
-      {
-        uint32_t a[32], bq[32];
-        tmem_ld32(t_dp, a);
-        tmem_ld32(t_dp + 32, bq);
-        tmem_ld_wait();
-        reg_fence32(a);
-        reg_fence32(bq);
-        uint32_t pk[32];
-#pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const int c = 2 * e;
-          const float d0 = __uint_as_float(c < 32 ? a[c] : bq[c - 32]) - dd;
-          const float d1 = __uint_as_float(c < 32 ? a[c + 1] : bq[c - 31]) - dd;
-          pk[e] = pack_bf16x2(pr[c] * d0, pr[c + 1] * d1);
+      // the next unit and its row statistics, ahead of this one's epilogue
+      BwdQUnit un;
+      float nl_n = 0.f, dd_n = 0.f;
+      int id_n = -1;
+      if (ok) {
+        if (lane == 0) id_n = next_unit(k + 1, true);
+        id_n = __shfl_sync(0xffffffffu, id_n, 0);
+        if (id_n >= 0) {
+          bwd_q_unit<CAUSAL, VARLEN, MASKS>(p, id_n, false, un);
+          nl_n = stat(p.nlse2, un);
+          dd_n = stat(p.dsum, un);
         }
-        tmem_st32(t_dp, pk);  // dS into the first 32 columns of this warpgroup's run
-        tmem_st_wait();
-        tc_fence_before_sync();
-        mbar_arrive(bar(C::QB_DSF));
       }
-    }
-    // ---- epilogue: each warpgroup writes half of the dQ row (times scale)
-    const bool have = NI > 0;
-    if (have && ok) {
-      ok = mbar_wait_warp(bar(C::QB_ACC), 0, abort_flag);
-      tc_fence_after_sync();
-    }
-    if ((!have || ok) && row0 < n_rows) {
-      constexpr int HALF = D / 2;
-      const uint32_t t_acc = tmem + lane_off + C::Q_TM_DQ + wg * HALF;
-      const int rr = row < n_rows ? row : 0;
-      uint16_t* out = p.dq +
-                      (VARLEN ? ((size_t)(sq.q0 + rr) * p.Hq + hq) : ((size_t)bh_q * p.Sq + rr)) * D +
-                      wg * HALF;
+      // ---- epilogue: each warpgroup writes half of the dQ row (times scale)
+      const bool have = NI > 0;
+      if (have && ok) {
+        ok = mbar_wait_warp(bar(C::QB_ACC), units & 1u, abort_flag);
+        ++units;
+        tc_fence_after_sync();
+      }
+      if (ok && u.row0 < u.n_rows) {
+        constexpr int HALF = D / 2;
+        const uint32_t t_acc = tmem + lane_off + C::Q_TM_DQ + wg * HALF;
+        const int rr = row < u.n_rows ? row : 0;
+        uint16_t* out = p.dq +
+                        (VARLEN ? ((size_t)(u.sq.q0 + rr) * p.Hq + u.hq)
+                                : ((size_t)u.bh_q * p.Sq + rr)) * D +
+                        wg * HALF;
 #pragma unroll
-      for (int c = 0; c < HALF; c += 32) {
-        uint32_t v[32];
-        if (have) {
-          tmem_ld32_sync(t_acc + c, v);
-        } else {
+        for (int c = 0; c < HALF; c += 32) {
+          uint32_t v[32];
+          if (have) {
+            tmem_ld32_sync(t_acc + c, v);
+          } else {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] = 0u;
+            for (int e = 0; e < 32; ++e) v[e] = 0u;
+          }
+          if (row < u.n_rows) bwd_store32(out + c, v, p.scale);
         }
-        if (row < n_rows) bwd_store32(out + c, v, p.scale);
       }
+      if (!ok) break;
+      tc_fence_before_sync();  // dQ read: the next unit's first dS (and so dQ) may follow
+      id = id_n;
+      u = un;
+      nl = nl_n;
+      dd = dd_n;
     }
   }
 
