@@ -814,17 +814,14 @@ __global__ void __launch_bounds__(384, 1)
   const bool masked = MASKS && p.block_mask != nullptr;
   const uint16_t* list = reinterpret_cast<const uint16_t*>(sbase_ptr + C::Q_OFF_LIST);
   int* list_count = reinterpret_cast<int*>(sbase_ptr + C::Q_OFF_MISC + 8);
-  bool listed = false;
-  if (masked) {
-    BwdQUnit u;
-    bwd_q_unit<CAUSAL, VARLEN, MASKS>(p, blockIdx.x, false, u);
-    listed = u.n > 0 && u.n <= C::LIST_MAX;
-    if (listed)
-      bwd_list_blocks(
-          u.n, [&](int c) { return bwd_block_on(p, u.b, u.hq, u.qt, u.kt_lo + c); },
-          reinterpret_cast<uint16_t*>(sbase_ptr + C::Q_OFF_LIST),
-          sbase_ptr + C::Q_OFF_LIST + 2 * C::LIST_MAX, list_count);
-  }
+  BwdQUnit u;  // every role's current unit; the CTA's own at first
+  bwd_q_unit<CAUSAL, VARLEN, MASKS>(p, blockIdx.x, threadIdx.x == 0, u);
+  const bool listed = masked && u.n > 0 && u.n <= C::LIST_MAX;
+  if (listed)
+    bwd_list_blocks(
+        u.n, [&](int c) { return bwd_block_on(p, u.b, u.hq, u.qt, u.kt_lo + c); },
+        reinterpret_cast<uint16_t*>(sbase_ptr + C::Q_OFF_LIST),
+        sbase_ptr + C::Q_OFF_LIST + 2 * C::LIST_MAX, list_count);
 
   if (threadIdx.x == 0) {
     mbar_init(bar(C::QB_QF), 1);
@@ -895,11 +892,9 @@ __global__ void __launch_bounds__(384, 1)
         ++q_loads;
         return true;
       };
-      int id = blockIdx.x;
-      for (int k = 0; ok && id >= 0; ++k) {
-        BwdQUnit u;
-        bwd_q_unit<CAUSAL, VARLEN, MASKS>(p, id, true, u);
+      for (int k = 0; ok; ++k) {
         const int NI = n_tiles(u);
+        if (k == 0 && NI > 0) load_q(u);
         for (int n = 0; n < NI; ++n) {
           const int s = kv % C::STAGES;
           if (kv >= C::STAGES &&
@@ -913,8 +908,8 @@ __global__ void __launch_bounds__(384, 1)
             tma_load_3d(sV(s) + cb * C::CB_BYTES, &tm_v, bar(C::QB_KVF + s), 64 * cb, ky, kz);
           }
           ++kv;
-          // Q and dO behind the first K and V: their buffers free later
-          if (n == 0 && !(ok = load_q(u))) break;
+          // a later unit's Q and dO behind its first K and V: their buffers free later
+          if (n == 0 && k > 0 && !(ok = load_q(u))) break;
         }
         if (!ok) break;
         if (!masked) {
@@ -927,7 +922,9 @@ __global__ void __launch_bounds__(384, 1)
           bwd_ask_next(slot(k + 1), bar(C::QB_NF + ((k + 1) & 1)));
           ++asked;
         }
-        id = next_unit(k + 1, false);
+        const int id = next_unit(k + 1, false);
+        if (id < 0) break;
+        bwd_q_unit<CAUSAL, VARLEN, MASKS>(p, id, true, u);
       }
       // Drain: no copy and no answer may still be on its way when the CTA exits.
       if (q_loads > 0) mbar_wait(bar(C::QB_QF), (q_loads - 1) & 1u, nullptr);
@@ -949,10 +946,7 @@ __global__ void __launch_bounds__(384, 1)
       };
       int it = 0, units = 0;
       bool ok = true;
-      int id = blockIdx.x;
-      for (int k = 0; ok && id >= 0; ++k) {
-        BwdQUnit u;
-        bwd_q_unit<CAUSAL, VARLEN, MASKS>(p, id, false, u);
+      for (int k = 0; ok; ++k) {
         const int NI = n_tiles(u);
         if (NI > 0) {
           const int s0 = it % C::STAGES;
@@ -1002,8 +996,11 @@ __global__ void __launch_bounds__(384, 1)
           if (!ok) break;
           ++units;
         }
+        int id = 0;
         if (lane == 0) id = next_unit(k + 1, true);
         id = __shfl_sync(0xffffffffu, id, 0);
+        if (id < 0) break;
+        bwd_q_unit<CAUSAL, VARLEN, MASKS>(p, id, false, u);
       }
       // every MMA issued above retires before TMEM is freed; an aborted unit's by a commit of
       // its own
@@ -1024,14 +1021,11 @@ __global__ void __launch_bounds__(384, 1)
     const uint64_t c2x2 = f32x2(p.scale_log2, p.scale_log2);
     int it = 0, units = 0;
     bool ok = true;
-    int id = blockIdx.x;
-    BwdQUnit u;
-    bwd_q_unit<CAUSAL, VARLEN, MASKS>(p, id, false, u);
     auto stat = [&](const float* x, const BwdQUnit& v) {
       return x[(size_t)v.bh_q * p.Sq_pad + v.row0 + r];
     };
     float nl = stat(p.nlse2, u), dd = stat(p.dsum, u);
-    for (int k = 0; id >= 0; ++k) {
+    for (int k = 0;; ++k) {
       const int NI = n_tiles(u);
       const int row = u.row0 + r;
       const uint64_t nlx2 = f32x2(nl, nl);
@@ -1145,9 +1139,8 @@ __global__ void __launch_bounds__(384, 1)
           if (row < u.n_rows) bwd_store32(out + c, v, p.scale);
         }
       }
-      if (!ok) break;
+      if (!ok || id_n < 0) break;
       tc_fence_before_sync();  // dQ read: the next unit's first dS (and so dQ) may follow
-      id = id_n;
       u = un;
       nl = nl_n;
       dd = dd_n;

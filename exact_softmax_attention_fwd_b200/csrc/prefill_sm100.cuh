@@ -648,12 +648,17 @@ __global__ void __launch_bounds__(384, 1)
         const uint64_t vd = smem_desc_sw128(opaque_u32(sbase + C::OFF_V + stage * C::TILE_BYTES), C::CB_BYTES, 1024);
         const uint32_t ts = opaque_u32(tmem + C::tmem_s(i));
         const uint32_t dt = tmem + C::tmem_o(i);
+        if (MASKS && narrow) {
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks) {
-          if (MASKS && narrow && ks >= kSinkCols / 16) break;
+          for (int ks = 0; ks < kSinkCols / 16; ++ks)
+            umma_ts(dt, ts + ks * 8, vd + (uint64_t)((ks * 2048) >> 4), idesc_pv,
+                    (accumulate || ks > 0) ? 1u : 0u);
+          return;
+        }
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks)
           umma_ts(dt, ts + ks * 8, vd + (uint64_t)((ks * 2048) >> 4), idesc_pv,
                   (accumulate || ks > 0) ? 1u : 0u);
-        }
       };
       uint32_t kv = 0;                  // ring position
       uint32_t q_waits0 = 0, q_waits1 = 0;  // Q_FULL phases consumed per tile slot
