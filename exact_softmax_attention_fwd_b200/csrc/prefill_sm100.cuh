@@ -58,6 +58,13 @@
 // O = o / l and LSE are unchanged in exact arithmetic because the same base
 // enters o and l.
 //
+// With a sliding window a few first tokens may stay visible ("sinks"): a unit's
+// stream is then the tiles of those tokens followed by the window's, and with up
+// to 32 of them their tile is computed as 32 columns.  Measured on 2 x 32 heads x
+// 8192 rows, d = 128, window 1024: 324 us without, 340 us with 4 first tokens
+// (760 TFLOP/s over visible pairs, 0.46 of the measured 1648), against 2.4 us a
+// step of two tiles, the pace of the causal kernel, whose softmax bounds it.
+//
 // Empty rows (no visible key) get O = 0 and LSE = -inf: the exponent base
 // falls back to 0 while the running max is -inf, so P = 2^-inf = 0 and l = 0.
 #pragma once

@@ -69,7 +69,9 @@ int rope_run(const void* q, const void* k, void* q_out, void* k_out, const doubl
              int rotary_dim, int interleaved, float mscale, const long long* strides,
              float sin_sign, attn_stream_t stream) {
   if (B < 1 || Hq < 1 || Hkv < 0 || S < 0 || inv_freq == nullptr) return ATTN_ERR_INVALID_ARG;
-  if (S > 0 && (q == nullptr || q_out == nullptr || (Hkv > 0 && (k == nullptr || k_out == nullptr))))
+  if (S > 0 && (q == nullptr || q_out == nullptr))
+    return ATTN_ERR_INVALID_ARG;
+  if (S > 0 && Hkv > 0 && (k == nullptr || k_out == nullptr))
     return ATTN_ERR_INVALID_ARG;
   if (B > (1 << 24) || S > (1 << 30) || (long long)B * S > 0x7fffffffLL || Hq > 32767 ||
       Hkv > 32767)

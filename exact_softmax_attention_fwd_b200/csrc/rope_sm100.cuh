@@ -165,7 +165,8 @@ __global__ void __launch_bounds__(kRopeThreads) attn_rope_kernel(const RopeParam
 #pragma unroll
     for (int i = 0; i < kRopeBatch; ++i) {
       if (h + i < h_end) {
-        uint16_t* dst = h + i < p.Hq ? q_dst + (h + i) * p.qos[1] : k_dst + (h + i - p.Hq) * p.kos[1];
+        uint16_t* dst =
+            h + i < p.Hq ? q_dst + (h + i) * p.qos[1] : k_dst + (h + i - p.Hq) * p.kos[1];
         if (turns) {
           float y[16];
           rope_turn<INTERLEAVED>(x0[i], x1[i], cs, sn, y);
@@ -186,6 +187,12 @@ __global__ void __launch_bounds__(kRopeThreads) attn_rope_kernel(const RopeParam
 // cu there is one token per sequence (decode), key number seq_lens[b] - 1.
 // K (and Q, when it is given) are rotated on the way; V is copied.  For an
 // E4M3 cache the values are divided by the page's scale and rounded once.
+// Measured: 8300 tokens x 48 heads of 128 in 8 chunks, 46.9 us (254 MB, 5.4 TB/s; an
+// elementwise kernel over as many contiguous bytes takes 38.9 us); 64 single
+// tokens 2.75 us, little more than a launch.  Its blocks begin with a chain of
+// dependent loads (offsets, length, block table); looking places up and sharing
+// angles through shared memory, for blocks that take whole tokens, measured 49 us
+// and 3.3 us.
 // ---------------------------------------------------------------------------
 struct AppendParams {
   const uint16_t* q;   // nullptr: no queries
