@@ -77,8 +77,9 @@ bool make_tile_map(CUtensorMap* map, const void* ptr, int D, long long rows, lon
 // 3-D bf16 map over a packed token-major [tokens, heads, D] tensor, box =
 // box_rows tokens of box_heads heads (one, unless said) x 64 columns, 128-byte
 // swizzle: with 128 rows in all the same shared-memory tile as make_tile_map
-// gives (128 rows of 128 bytes); a paged pool [num_pages, page_size, heads, D] is such a tensor with
-// num_pages * page_size tokens, read one page (box_rows = page_size) at a time.
+// gives (128 rows of 128 bytes); a paged pool [num_pages, page_size, heads, D]
+// is such a tensor with num_pages * page_size tokens, read one page (box_rows =
+// page_size) at a time.
 bool make_token_map(CUtensorMap* map, const void* ptr, int D, long long heads, long long tokens,
                     unsigned box_rows = 128, unsigned box_heads = 1) {
   const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)tokens};
@@ -691,8 +692,9 @@ size_t bwd_workspace_bytes(int B, int Hq, int Sq) {
 // How the first tokens' far query tiles (those that see a key tile through its
 // first tokens alone) are dealt to units of the dK/dV kernel: chunks per key
 // tile, as long as an ordinary unit (the window's query tiles of the group),
-// but no more units than four for every SM, which also bounds the partial
-// sums' memory.  0 chunks: no query tile is far.
+// but no more units than four for every SM (148 on a B200), which also bounds
+// the partial sums' memory.  0 chunks: no query tile is far, or one chunk would
+// do, and the key tile's own unit walks them as well.
 struct BwdFar {
   int tiles, chunks, rows;
   size_t bytes;  // of partial sums
@@ -712,8 +714,10 @@ BwdFar bwd_far(int B, int Hq, int Hkv, int Sq, int Sk, int d, int window, int si
   f.tiles = (f.rows + 127) / 128;
   const long long unit = group * ((long long)window / 128 + 2);
   const long long by_length = (group * (n_qt - near_qt) + unit - 1) / unit;
-  const long long by_count = std::max(1ll, 4 * 148 / (f.tiles * bh));
-  f.chunks = (int)std::min(by_length, by_count);
+  const long long by_count = 4 * 148 / (f.tiles * bh);
+  const long long chunks = std::min(by_length, by_count);
+  if (chunks < 2) return BwdFar{0, 0, 0, 0};
+  f.chunks = (int)chunks;
   f.bytes = (size_t)(f.chunks + 1) * bh * f.rows * 2 * d * sizeof(float);
   return f;
 }

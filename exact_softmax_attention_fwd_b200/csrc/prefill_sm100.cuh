@@ -269,8 +269,9 @@ __device__ __forceinline__ bool prefill_unit(const PrefillParams& p, int k, Pref
     u.b = e.x;
     u.qb = e.y;
     u.q_tok0 = __ldg(p.cu_q + u.b);
-    u.sq = (__ldg(p.cu_q + u.b + 1) - u.q_tok0) << (PACKS ? p.pack : 0);  // listed sequences passed the
-    if (LAYOUT == kLayoutPaged) {                  // schedule kernel's checks
+    // listed sequences passed the schedule kernel's checks
+    u.sq = (__ldg(p.cu_q + u.b + 1) - u.q_tok0) << (PACKS ? p.pack : 0);
+    if (LAYOUT == kLayoutPaged) {
       u.k_tok0 = 0;
       u.klen = __ldg(p.seq_lens_k + u.b);
     } else {
