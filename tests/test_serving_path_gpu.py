@@ -206,3 +206,38 @@ def test_training_step_gradients(interleaved):
         # (dS meets the rounded operand) and 2.3e-3 of the norm
         g, w = S.f64(g), np.asarray(w)
         assert np.linalg.norm(g - w) <= math.sqrt(5e-3 ** 2 + 2 * 2.3e-3 ** 2) * np.linalg.norm(w), name
+
+
+def test_two_streams_at_once():
+    """The same calls on two streams with work of different sizes in flight together, many times:
+    the bits of each stream's results are those of the calls alone (units that a CTA takes over,
+    clusters and workspaces belong to their own launch)."""
+    def work(seed, n, window):
+        q, k, v = (x.to(DEV) for x in W.prefill_inputs(1, 8, 2, n, n, 128, seed))
+        do = W.grad_output(1, 8, n, 128, seed).to(DEV)
+        c = W.paged_inputs(torch.tensor([n, 33, 700], dtype=torch.int32), 8, 2, 128, 16, seed)
+        paged = [x.to(DEV) for x in (c.q, c.k_cache, c.v_cache, c.block_table, c.seq_lens)]
+        freq = rope_frequencies(128)[0].to(DEV)
+
+        def run(stream):
+            a, b = attn_rope(q, k, freq, stream=stream)
+            o, lse = attn_fwd_window_sinks(a, b, v, 0.088, window, 4, stream=stream)
+            grads = attn_bwd_window_sinks(a, b, v, o, lse, do, 0.088, window, 4, stream=stream)
+            return (o, lse) + grads + attn_decode_paged_window(*paged, 0.088, window, 4, stream=stream)
+
+        return run
+
+    calls = [work(311, 3000, 200), work(312, 900, 64)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    want = []
+    for call, s in zip(calls, streams):
+        torch.cuda.synchronize()
+        want.append(call(s))
+        torch.cuda.synchronize()
+    for _ in range(10):
+        got = [[call(s) for _ in range(3)] for call, s in zip(calls, streams)]
+        torch.cuda.synchronize()
+        for runs, ref in zip(got, want):
+            for r in runs:
+                assert all(torch.equal(x, y) for x, y in zip(r, ref))
+    _ok()
