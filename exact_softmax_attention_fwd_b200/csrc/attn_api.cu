@@ -262,8 +262,8 @@ template <int D, bool CAUSAL, bool VARLEN = false, bool MASKS = false>
 int launch_bwd(const CUtensorMap& mq, const CUtensorMap& mdo, const CUtensorMap& mk,
                const CUtensorMap& mv, const BwdParams& prm, cudaStream_t stream) {
   using C = BwdCfg<D>;
-  const long long prep_threads = (long long)prm.B * prm.Hq * prm.Sq_pad * (D / 8);
-  const long long prep_blocks = (prep_threads + 255) / 256;
+  const long long prep_blocks =
+      (long long)prm.B * prm.Hq * (prm.Sq_pad / (kPrepRows * 256 / (D / 8)));
   const long long kv_units =
       ((long long)prm.n_kt + (long long)prm.far_tiles * prm.far_chunks) * prm.B * prm.Hkv;
   const long long q_units = (long long)prm.n_qt * prm.B * prm.Hq;

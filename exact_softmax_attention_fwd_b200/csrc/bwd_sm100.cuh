@@ -237,47 +237,58 @@ __device__ __forceinline__ float bwd_keep(bool visible, float x) {
 }
 
 // D = rowsum(dO * O) and -LSE*log2(e) for every padded query row.  D/8
-// threads per row, 8 elements each, reduced by shuffles.
+// threads per row, 8 elements each, reduced by shuffles; a thread has the pieces
+// of 4 rows in flight, and a block's rows lie in one (sequence, head), whose
+// place is worked out once (one row a thread, found by 64-bit divisions, took
+// 26.8 us for 32 x 8192 rows of 128, 134 MB).
+constexpr int kPrepRows = 4;  // rows a thread has in flight
+
 template <int D, bool VARLEN>
 __global__ void __launch_bounds__(256) attn_bwd_prep_kernel(const BwdParams p) {
   constexpr int TPR = D / 8;
-  const long long n_rows = (long long)p.B * p.Hq * p.Sq_pad;
-  const long long gt = (long long)blockIdx.x * blockDim.x + threadIdx.x;
-  const long long row = gt / TPR;
-  const int part = (int)(gt % TPR);
-  const bool valid = row < n_rows;
-  const long long bh = valid ? row / p.Sq_pad : 0;
-  const int i = valid ? (int)(row % p.Sq_pad) : 0;
+  constexpr int STEP = 256 / TPR;              // rows the block takes at a time
+  constexpr int ROWS = kPrepRows * STEP;       // of the block: 64 or 128, a divisor of Sq_pad
+  const unsigned per_bh = (unsigned)(p.Sq_pad / ROWS);
+  const int bh = (int)(blockIdx.x / per_bh);
+  const int i0 = (int)(blockIdx.x % per_bh) * ROWS + (int)threadIdx.x / TPR;
+  const int part = threadIdx.x % TPR;
+  const int b = bh / p.Hq, h = bh % p.Hq;
   BwdSeq sq;
-  const int b = (int)(bh / p.Hq), h = (int)(bh % p.Hq);
-  const bool seq_ok = valid && bwd_sequence<VARLEN>(p, b, false, sq);
-  const bool live = seq_ok && i < sq.lq;
-  // dense: [B*Hq, Sq] rows; ragged: token q0 + i of head h in [total_q, Hq]
-  const size_t row_el = VARLEN ? ((size_t)(sq.q0 + i) * p.Hq + h) : ((size_t)bh * p.Sq + i);
-  const size_t lse_at = VARLEN ? ((size_t)h * p.total_q + sq.q0 + i) : ((size_t)bh * p.Sq + i);
-  float acc = 0.f;
-  if (live) {
-    const size_t off = row_el * D + part * 8;
-    const uint4 a = ld_stream_v4(p.d_o + off);
-    const uint4 b = ld_stream_v4(p.o + off);
-    const uint32_t aw[4] = {a.x, a.y, a.z, a.w};
-    const uint32_t bw[4] = {b.x, b.y, b.z, b.w};
+  const bool seq_ok = bwd_sequence<VARLEN>(p, b, false, sq);
+  uint4 x[kPrepRows], y[kPrepRows];
+  float l[kPrepRows];
+#pragma unroll
+  for (int k = 0; k < kPrepRows; ++k) {
+    const int i = i0 + k * STEP;
+    x[k] = y[k] = make_uint4(0u, 0u, 0u, 0u);
+    l[k] = -INFINITY;
+    if (seq_ok && i < sq.lq) {
+      // dense: [B*Hq, Sq] rows; ragged: token q0 + i of head h in [total_q, Hq]
+      const size_t row_el = VARLEN ? ((size_t)(sq.q0 + i) * p.Hq + h) : ((size_t)bh * p.Sq + i);
+      const size_t off = row_el * D + part * 8;
+      x[k] = ld_stream_v4(p.d_o + off);
+      y[k] = ld_stream_v4(p.o + off);
+      if (part == 0)
+        l[k] = p.lse[VARLEN ? ((size_t)h * p.total_q + sq.q0 + i) : ((size_t)bh * p.Sq + i)];
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kPrepRows; ++k) {
+    const uint32_t aw[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+    const uint32_t bw[4] = {y[k].x, y[k].y, y[k].z, y[k].w};
+    float acc = 0.f;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       acc = fmaf(__uint_as_float(aw[e] << 16), __uint_as_float(bw[e] << 16), acc);
       acc = fmaf(__uint_as_float(aw[e] & 0xFFFF0000u), __uint_as_float(bw[e] & 0xFFFF0000u), acc);
     }
-  }
 #pragma unroll
-  for (int w = TPR / 2; w >= 1; w >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, w);
-  if (valid && part == 0) {
-    float nl = -INFINITY;
-    if (live) {
-      const float l = p.lse[lse_at];
-      nl = (l == -INFINITY) ? -INFINITY : -l * 1.4426950408889634f;
+    for (int w = TPR / 2; w >= 1; w >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, w);
+    if (part == 0) {
+      const size_t row = (size_t)bh * p.Sq_pad + i0 + k * STEP;
+      p.nlse2[row] = l[k] == -INFINITY ? -INFINITY : -l[k] * 1.4426950408889634f;
+      p.dsum[row] = acc;  // rows past the sequence: 0
     }
-    p.nlse2[row] = nl;
-    p.dsum[row] = live ? acc : 0.f;
   }
 }
 
