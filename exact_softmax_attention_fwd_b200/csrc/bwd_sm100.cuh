@@ -292,11 +292,18 @@ __global__ void __launch_bounds__(256) attn_bwd_prep_kernel(const BwdParams p) {
   }
 }
 
-// SS MMA over the head dimension: D[tm] = A B^T, A and B 128-row K-major tiles.
-template <int D>
+// Columns of the dQ kernel's tile of visible first tokens that are computed, when
+// there are no more of them than that and the window leaves a gap behind them
+// (32 x 8192 rows, window 1024, 4 first tokens: the backward takes 574 us with all
+// 128 columns, 560 us so).
+constexpr int kBwdSinkCols = 32;
+
+// SS MMA over the head dimension: D[tm] = A B^T, A and B 128-row K-major tiles
+// (of B, the first N rows).
+template <int D, int N = 128>
 __device__ __forceinline__ void bwd_mma_ss(uint32_t d_tmem, uint32_t a, uint32_t b) {
   using C = BwdCfg<D>;
-  constexpr uint32_t idesc = idesc_bf16_f32(128, 128, false);
+  constexpr uint32_t idesc = idesc_bf16_f32(128, N, false);
 #pragma unroll
   for (int ks = 0; ks < D / 16; ++ks) {
     const uint32_t off = (ks >> 2) * C::CB_BYTES + (ks & 3) * 32;
@@ -307,14 +314,14 @@ __device__ __forceinline__ void bwd_mma_ss(uint32_t d_tmem, uint32_t a, uint32_t
 
 // TS MMA over 128 rows: D[tm] (+)= A B with A [128 x 128] bf16 in TMEM (its
 // columns 0-31 and 64-95: the two warpgroups' packed runs) and B a 128-row tile
-// used MN-major (its rows are the reduction index).
-template <int D>
+// used MN-major (its rows are the reduction index, the first K of them).
+template <int D, int K = 128>
 __device__ __forceinline__ void bwd_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b,
                                            bool accumulate) {
   using C = BwdCfg<D>;
   constexpr uint32_t idesc = idesc_bf16_f32(128, D, true);
 #pragma unroll
-  for (int ks = 0; ks < 8; ++ks) {
+  for (int ks = 0; ks < K / 16; ++ks) {
     umma_ts(d_tmem, a_tmem + (ks >> 2) * 64 + (ks & 3) * 8,
             smem_desc_sw128(b + ks * 2048, C::CB_BYTES, 1024), idesc,
             (accumulate || ks > 0) ? 1u : 0u);
@@ -744,6 +751,7 @@ struct BwdQUnit {
   int b, hq, kvh, bh_q, bh_kv, qt, row0, klen, n_rows;
   long long koff;
   int kt_lo, st, n;  // key tiles walked: [0, st) (first tokens), then from kt_lo on; n in all
+  bool narrow;       // the first of them as kBwdSinkCols columns
 };
 
 template <bool CAUSAL, bool VARLEN, bool MASKS>
@@ -778,6 +786,7 @@ __device__ __forceinline__ void bwd_q_unit(const BwdParams& p, int id, bool repo
     u.st = (min(p.sinks, u.klen) + 127) / 128;
     if (u.kt_lo <= u.st) u.kt_lo = u.st = 0;
   }
+  u.narrow = MASKS && u.st > 0 && p.sinks <= kBwdSinkCols;
   u.n = (u.row0 >= u.n_rows || kt_end <= u.kt_lo) ? 0 : u.st + kt_end - u.kt_lo;
 }
 
@@ -973,9 +982,15 @@ __global__ void __launch_bounds__(384, 1)
             break;
           tc_fence_after_sync();
           if (elect_one()) {
-            bwd_mma_ss<D>(tS(it), sQ, sK(s0));
-            umma_commit(bar(C::QB_SF + (it & 1)));
-            bwd_mma_ss<D>(tDP, sDO, sV(s0));
+            if (MASKS && u.narrow) {
+              bwd_mma_ss<D, kBwdSinkCols>(tS(it), sQ, sK(s0));
+              umma_commit(bar(C::QB_SF + (it & 1)));
+              bwd_mma_ss<D, kBwdSinkCols>(tDP, sDO, sV(s0));
+            } else {
+              bwd_mma_ss<D>(tS(it), sQ, sK(s0));
+              umma_commit(bar(C::QB_SF + (it & 1)));
+              bwd_mma_ss<D>(tDP, sDO, sV(s0));
+            }
             umma_commit(bar(C::QB_DPF));
             if (NI == 1) umma_commit(bar(C::QB_QE));
           }
@@ -996,7 +1011,10 @@ __global__ void __launch_bounds__(384, 1)
             if (elect_one()) {
               // dQ += dS K.  A unit's first one overwrites the last unit's dQ, which
               // was stored before its threads wrote this dS.
-              bwd_mma_ts<D>(tDQ, tDP, sK(s), n > 0);
+              if (MASKS && u.narrow && n == 0)
+                bwd_mma_ts<D, kBwdSinkCols>(tDQ, tDP, sK(s), false);
+              else
+                bwd_mma_ts<D>(tDQ, tDP, sK(s), n > 0);
               umma_commit(bar(C::QB_KVE + s));
               if (n + 1 < NI) {
                 // dP of the next key tile: overwrites dS only after the MMA above read it
@@ -1051,6 +1069,39 @@ __global__ void __launch_bounds__(384, 1)
         kend = min(kend, max((long long)row + u.koff, MASKS ? (long long)p.prefix - 1 : -1LL) + 1);
       if (MASKS && p.window > 0) klo = max(0LL, (long long)row + u.koff - p.window + 1);
       for (int n = 0; n < NI; ++n, ++it) {
+        if (MASKS && u.narrow && n == 0) {
+          // the first tokens' columns, which every row here sees: all in the first
+          // warpgroup's run; the second one only keeps step
+          const uint32_t vis = low_bits(p.sinks);
+          if (!(ok = mbar_wait_warp(bar(C::QB_SF + (it & 1)), (it >> 1) & 1u, abort_flag))) break;
+          tc_fence_after_sync();
+          uint32_t x[32];
+          if (wg == 0) {
+            tmem_ld32_sync(tmem + lane_off + ((it & 1) ? C::Q_TM_S1 : C::Q_TM_S0), x);
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              x[c] = (vis & (1u << c))
+                         ? __float_as_uint(ex2(fmaf(__uint_as_float(x[c]), p.scale_log2, nl)))
+                         : 0u;
+          }
+          if (!(ok = mbar_wait_warp(bar(C::QB_DPF), it & 1u, abort_flag))) break;
+          tc_fence_after_sync();
+          if (wg == 0) {
+            uint32_t a[32], pk[16];
+            tmem_ld32_sync(t_dp, a);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float d0 = __uint_as_float(a[2 * e]) - dd;
+              const float d1 = __uint_as_float(a[2 * e + 1]) - dd;
+              pk[e] = pack_bf16x2(__uint_as_float(x[2 * e]) * d0, __uint_as_float(x[2 * e + 1]) * d1);
+            }
+            tmem_st16(t_dp, pk);
+            tmem_st_wait();
+          }
+          tc_fence_before_sync();
+          mbar_arrive(bar(C::QB_DSF));
+          continue;
+        }
         const int kt = key_tile(u, n);
         const long long t0 = (long long)kt * 128 + c0;  // this run's first key
         long long cm = kend - t0;  // visible iff cmin <= c < cmax
