@@ -416,15 +416,11 @@ __global__ void __launch_bounds__(384, 1)
   const bool listed = MASKS && p.block_mask != nullptr && N > 0 && N <= C::LIST_MAX;
   const uint16_t* list = reinterpret_cast<const uint16_t*>(sbase_ptr + C::KV_OFF_LIST);
   int* list_count = reinterpret_cast<int*>(sbase_ptr + C::KV_OFF_MISC + 8);
-  if (listed)
-    bwd_list_blocks(
-        N, [&](int c) { return bwd_block_on(p, b, kvh * p.group + c / nq, qt_lo + c % nq, kb); },
-        reinterpret_cast<uint16_t*>(sbase_ptr + C::KV_OFF_LIST),
-        sbase_ptr + C::KV_OFF_LIST + 2 * C::LIST_MAX, list_count);
   // dK/dV rows this CTA writes: a ragged sequence's own keys only (rows past
   // them belong to the next sequence); fixed-length batches write every key
   // row of the tile (padded keys get zeros)
   const int key_rows = VARLEN ? (seq_ok ? sq.lk : 0) : p.Sk;
+  const uint32_t sK = sbase + C::KV_OFF_K, sV = sbase + C::KV_OFF_V;
 
   if (threadIdx.x == 0) {
     mbar_init(bar(C::KB_KV), 1);
@@ -440,30 +436,9 @@ __global__ void __launch_bounds__(384, 1)
     *abort_flag = 0;
     mbar_init_fence();
     fence_proxy_async_smem();
-  }
-  if (warp == 1) {
-    tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
-    tmem_relinquish();
-  }
-  tc_fence_before_sync();
-  __syncthreads();
-  tc_fence_after_sync();
-  const uint32_t tmem = *tmem_slot;
-  const int NI = listed ? *list_count : N;  // iterations walked
-  auto cand = [&](int n) { return listed ? (int)list[n] : n + c_lo; };
-  const uint32_t sK = sbase + C::KV_OFF_K, sV = sbase + C::KV_OFF_V;
-  auto sQ = [&](int s) { return sbase + C::KV_OFF_Q + (uint32_t)s * C::TILE_BYTES; };
-  auto sDO = [&](int s) { return sbase + C::KV_OFF_DO + (uint32_t)s * C::TILE_BYTES; };
-  auto sST = [&](int s) { return sbase + C::KV_OFF_ST + (uint32_t)s * C::STAT_BYTES; };
-
-  if (warp < 4) {
-    warpgroup_reg_dealloc<C::REGS_PRODUCER>();
-    if (warp == 0 && lane == 0 && NI > 0) {
-      // ======================= TMA producer =======================
-      tma_prefetch_map(&tm_q);
-      tma_prefetch_map(&tm_do);
-      tma_prefetch_map(&tm_k);
-      tma_prefetch_map(&tm_v);
+    // K and V travel while the blocks are listed and TMEM is allocated (32 x 8192 rows,
+    // block mask of density 0.25: dK/dV 535 -> 528 us, dQ with its Q and dO 522 -> 515)
+    if (N > 0) {
       mbar_arrive_expect_tx(bar(C::KB_KV), 2 * C::TILE_BYTES);
       // fixed-length maps are (d, S, B*H); ragged ones (d, H, tokens)
       for (int cb = 0; cb < C::NCB; ++cb) {
@@ -472,6 +447,33 @@ __global__ void __launch_bounds__(384, 1)
         tma_load_3d(sV + cb * C::CB_BYTES, &tm_v, bar(C::KB_KV), 64 * cb, VARLEN ? kvh : key0,
                     VARLEN ? sq.k0 + key0 : bh_kv);
       }
+      tma_prefetch_map(&tm_q);
+      tma_prefetch_map(&tm_do);
+    }
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  if (listed)
+    bwd_list_blocks(
+        N, [&](int c) { return bwd_block_on(p, b, kvh * p.group + c / nq, qt_lo + c % nq, kb); },
+        reinterpret_cast<uint16_t*>(sbase_ptr + C::KV_OFF_LIST),
+        sbase_ptr + C::KV_OFF_LIST + 2 * C::LIST_MAX, list_count);
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  const int NI = listed ? *list_count : N;  // iterations walked
+  auto cand = [&](int n) { return listed ? (int)list[n] : n + c_lo; };
+  auto sQ = [&](int s) { return sbase + C::KV_OFF_Q + (uint32_t)s * C::TILE_BYTES; };
+  auto sDO = [&](int s) { return sbase + C::KV_OFF_DO + (uint32_t)s * C::TILE_BYTES; };
+  auto sST = [&](int s) { return sbase + C::KV_OFF_ST + (uint32_t)s * C::STAT_BYTES; };
+
+  if (warp < 4) {
+    warpgroup_reg_dealloc<C::REGS_PRODUCER>();
+    if (warp == 0 && lane == 0 && N > 0) {
+      // ======================= TMA producer =======================
       int issued = 0;
       bool ok = true;
       for (int n = 0; n < NI; ++n) {
@@ -842,11 +844,16 @@ __global__ void __launch_bounds__(384, 1)
   BwdQUnit u;  // every role's current unit; the CTA's own at first
   bwd_q_unit<CAUSAL, VARLEN, MASKS>(p, blockIdx.x, threadIdx.x == 0, u);
   const bool listed = masked && u.n > 0 && u.n <= C::LIST_MAX;
-  if (listed)
-    bwd_list_blocks(
-        u.n, [&](int c) { return bwd_block_on(p, u.b, u.hq, u.qt, u.kt_lo + c); },
-        reinterpret_cast<uint16_t*>(sbase_ptr + C::Q_OFF_LIST),
-        sbase_ptr + C::Q_OFF_LIST + 2 * C::LIST_MAX, list_count);
+  const uint32_t sQ = sbase + C::Q_OFF_Q, sDO = sbase + C::Q_OFF_DO;
+  auto load_q = [&](const BwdQUnit& u) {
+    mbar_arrive_expect_tx(bar(C::QB_QF), 2 * C::TILE_BYTES);
+    const int qy = VARLEN ? u.hq : u.row0, qz = VARLEN ? u.sq.q0 + u.row0 : u.bh_q;
+    for (int cb = 0; cb < C::NCB; ++cb) {
+      tma_load_3d(sQ + cb * C::CB_BYTES, &tm_q, bar(C::QB_QF), 64 * cb, qy, qz);
+      tma_load_3d(sDO + cb * C::CB_BYTES, &tm_do, bar(C::QB_QF), 64 * cb, qy, qz);
+    }
+  };
+  const bool own = u.n > 0;  // the CTA's own unit has key tiles (before any block mask)
 
   if (threadIdx.x == 0) {
     mbar_init(bar(C::QB_QF), 1);
@@ -866,11 +873,19 @@ __global__ void __launch_bounds__(384, 1)
     *abort_flag = 0;
     mbar_init_fence();
     fence_proxy_async_smem();
+    if (own) load_q(u);  // travels while the blocks are listed and TMEM is allocated
+    tma_prefetch_map(&tm_k);
+    tma_prefetch_map(&tm_v);
   }
   if (warp == 1) {
     tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
     tmem_relinquish();
   }
+  if (listed)
+    bwd_list_blocks(
+        u.n, [&](int c) { return bwd_block_on(p, u.b, u.hq, u.qt, u.kt_lo + c); },
+        reinterpret_cast<uint16_t*>(sbase_ptr + C::Q_OFF_LIST),
+        sbase_ptr + C::Q_OFF_LIST + 2 * C::LIST_MAX, list_count);
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
@@ -891,7 +906,6 @@ __global__ void __launch_bounds__(384, 1)
     if (frees) mbar_arrive(bar(C::QB_NE + (k & 1)));
     return id;
   };
-  const uint32_t sQ = sbase + C::Q_OFF_Q, sDO = sbase + C::Q_OFF_DO;
   auto sK = [&](int s) { return sbase + C::Q_OFF_K + (uint32_t)s * C::TILE_BYTES; };
   auto sV = [&](int s) { return sbase + C::Q_OFF_V + (uint32_t)s * C::TILE_BYTES; };
 
@@ -899,27 +913,12 @@ __global__ void __launch_bounds__(384, 1)
     warpgroup_reg_dealloc<C::REGS_PRODUCER>();
     if (warp == 0 && lane == 0) {
       // ======================= TMA producer =======================
-      tma_prefetch_map(&tm_q);
-      tma_prefetch_map(&tm_do);
-      tma_prefetch_map(&tm_k);
-      tma_prefetch_map(&tm_v);
-      int q_loads = 0, kv = 0;  // Q and dO, and K and V tiles, issued so far
-      int asked = 0;            // requests for a next unit issued so far
+      int q_loads = own ? 1 : 0;  // Q and dO tiles issued so far
+      int kv = 0;                 // K and V tiles
+      int asked = 0;              // requests for a next unit
       bool ok = true;
-      auto load_q = [&](const BwdQUnit& u) -> bool {
-        if (q_loads > 0 && !mbar_wait(bar(C::QB_QE), (q_loads - 1) & 1u, abort_flag)) return false;
-        mbar_arrive_expect_tx(bar(C::QB_QF), 2 * C::TILE_BYTES);
-        const int qy = VARLEN ? u.hq : u.row0, qz = VARLEN ? u.sq.q0 + u.row0 : u.bh_q;
-        for (int cb = 0; cb < C::NCB; ++cb) {
-          tma_load_3d(sQ + cb * C::CB_BYTES, &tm_q, bar(C::QB_QF), 64 * cb, qy, qz);
-          tma_load_3d(sDO + cb * C::CB_BYTES, &tm_do, bar(C::QB_QF), 64 * cb, qy, qz);
-        }
-        ++q_loads;
-        return true;
-      };
       for (int k = 0; ok; ++k) {
         const int NI = n_tiles(u);
-        if (k == 0 && NI > 0) load_q(u);
         for (int n = 0; n < NI; ++n) {
           const int s = kv % C::STAGES;
           if (kv >= C::STAGES &&
@@ -934,7 +933,12 @@ __global__ void __launch_bounds__(384, 1)
           }
           ++kv;
           // a later unit's Q and dO behind its first K and V: their buffers free later
-          if (n == 0 && k > 0 && !(ok = load_q(u))) break;
+          if (n == 0 && k > 0) {
+            if (q_loads > 0 && !(ok = mbar_wait(bar(C::QB_QE), (q_loads - 1) & 1u, abort_flag)))
+              break;
+            load_q(u);
+            ++q_loads;
+          }
         }
         if (!ok) break;
         if (!masked) {
