@@ -288,24 +288,25 @@ __global__ void __launch_bounds__(kWinWarps * 32, DecodeWinCfg<D, FP8>::CTAS4)
     auto part = [&](int i) { return reinterpret_cast<const float*>(sptr + i * W::RING); };
     for (int e = threadIdx.x * 4; e < p.group * D; e += blockDim.x * 4) {
       const int h = e / D;
-      float m[kWinWarps], mx = -INFINITY;
+      float m[kWinWarps], ls[kWinWarps], mx = -INFINITY;
 #pragma unroll
       for (int i = 0; i < kWinWarps; ++i) {
         m[i] = i < n_warps ? part(i)[8 * D + h] : -INFINITY;
+        ls[i] = i < n_warps ? part(i)[8 * D + 8 + h] : 0.f;
         mx = fmaxf(mx, m[i]);
       }
       float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
       float l = 0.f, lr = 0.f;
 #pragma unroll
       for (int i = 0; i < kWinWarps; ++i) {
-        if (m[i] == -INFINITY) continue;  // saw nothing
+        if (ls[i] == 0.f) continue;  // saw nothing (scores of NaN leave m at -inf, but l NaN)
         const float f = ex2(m[i] - mx);
         const float4 x = *reinterpret_cast<const float4*>(part(i) + e);
         sum.x = fmaf(f, x.x, sum.x);
         sum.y = fmaf(f, x.y, sum.y);
         sum.z = fmaf(f, x.z, sum.z);
         sum.w = fmaf(f, x.w, sum.w);
-        l = fmaf(f, part(i)[8 * D + 8 + h], l);
+        l = fmaf(f, ls[i], l);
         lr = fmaf(f, part(i)[8 * D + 16 + h], lr);
       }
       *reinterpret_cast<float4*>(out + e) = sum;
@@ -324,34 +325,35 @@ __global__ void __launch_bounds__(kWinWarps * 32, DecodeWinCfg<D, FP8>::CTAS4)
     for (int e = (rank * (int)blockDim.x + (int)threadIdx.x) * 4; e < p.group * D;
          e += n_threads * 4) {
       const int h = e / D;
-      float m[8], mx = -INFINITY;
+      float m[8], ls[8], mx = -INFINITY;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         m[i] = i < cs ? cluster_ld(cluster_map(local + (8 * D + h) * 4, i)) : -INFINITY;
+        ls[i] = i < cs ? cluster_ld(cluster_map(local + (8 * D + 8 + h) * 4, i)) : 0.f;
         mx = fmaxf(mx, m[i]);
       }
       float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
       float l = 0.f, lr = 0.f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        if (i >= cs || m[i] == -INFINITY) continue;
+        if (ls[i] == 0.f) continue;
         const float f = ex2(m[i] - mx);
         const float4 x = cluster_ld4(cluster_map(local + e * 4, i));
         sum.x = fmaf(f, x.x, sum.x);
         sum.y = fmaf(f, x.y, sum.y);
         sum.z = fmaf(f, x.z, sum.z);
         sum.w = fmaf(f, x.w, sum.w);
-        l = fmaf(f, cluster_ld(cluster_map(local + (8 * D + 8 + h) * 4, i)), l);
+        l = fmaf(f, ls[i], l);
         lr = fmaf(f, cluster_ld(cluster_map(local + (8 * D + 16 + h) * 4, i)), lr);
       }
-      const float inv = lr > 0.f ? 1.f / lr : 0.f;
+      const float inv = lr == 0.f ? 0.f : 1.f / lr;
       const size_t row = (size_t)b * p.Hq + hq0 + h;
       uint2 o;
       o.x = pack_bf16x2(sum.x * inv, sum.y * inv);
       o.y = pack_bf16x2(sum.z * inv, sum.w * inv);
       *reinterpret_cast<uint2*>(p.o + row * D + e % D) = o;
       if (p.lse != nullptr && e % D == 0)
-        p.lse[row] = l > 0.f ? (mx + lg2(l)) * 0.69314718055994531f : -INFINITY;
+        p.lse[row] = l == 0.f ? -INFINITY : (mx + lg2(l)) * 0.69314718055994531f;
     }
   }
   cluster_sync();  // no CTA leaves while another may read its part

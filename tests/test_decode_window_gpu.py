@@ -2,6 +2,7 @@
 first tokens (bf16 and E4M3 caches) against the float64 oracle, at the bar of
 tests/window_parity.py (the E4M3 kernel rounds its weights to f16, finer than the bar's bf16)."""
 import math
+from dataclasses import replace
 
 import pytest
 import torch
@@ -109,6 +110,29 @@ def test_slots_that_are_not_visible_may_hold_anything(fp8):
     o, lse = _call(c, 0.1, window, sinks, fp8, kc=kc, vc=vc, table=table)
     _ok()
     check_rows(o, lse, _ref(c, 0.1, window, sinks, fp8))
+
+
+@pytest.mark.parametrize("B_,window,sinks", [(1, 0, 0), (1, 200, 4), (40, 200, 4)])
+@pytest.mark.parametrize("where", ["query", "keys"])
+def test_nan_in_what_a_row_sees_reaches_its_result(where, B_, window, sinks):
+    """A query of NaN, or a run of visible keys of NaN (all that some warps see): the rows that
+    see them are NaN, O and LSE, and the others as ever."""
+    c = _make([500] + [300] * (B_ - 1), 4, 2, 64, 16, 216, False)
+    o0, lse0 = _call(c, 0.2, window, sinks, False)
+    q, kc = c.q.clone(), c.k_cache.clone()
+    hit = torch.zeros(B_, 4, dtype=torch.bool)
+    if where == "query":
+        q[0, 2] = float("nan")
+        hit[0, 2] = True
+    else:
+        for t in range(448, 480, 16):
+            kc[int(c.block_table[0, t // 16]), :, 1] = float("nan")
+        hit[0, 2:] = True
+    o, lse = _call(replace(c, q=q), 0.2, window, sinks, False, kc=kc)
+    _ok()
+    assert torch.isnan(o.cpu()[hit]).all() and torch.isnan(lse.cpu()[hit]).all()
+    assert torch.equal(o.cpu()[~hit], o0.cpu()[~hit])
+    assert torch.equal(lse.cpu()[~hit], lse0.cpu()[~hit])
 
 
 @pytest.mark.parametrize("fp8", [False, True])
