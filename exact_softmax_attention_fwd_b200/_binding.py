@@ -991,6 +991,8 @@ def _workspace(t, like, need, stream):
     import torch
     if t is None:
         t = _new(like, (max(need, 16),), torch.uint8, stream)
+    elif not t.is_contiguous():
+        raise ValueError("workspace must be contiguous")
     return t.data_ptr(), t.numel() * t.element_size(), t
 
 

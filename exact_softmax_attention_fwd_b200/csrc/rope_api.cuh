@@ -98,6 +98,10 @@ int rope_run(const void* q, const void* k, void* q_out, void* k_out, const doubl
     if (bad != ATTN_OK) return bad;
     if (t >= 2 && S > 0 && !rope_rows_apart(to[t], ext, d)) return ATTN_ERR_INVALID_ARG;
   }
+  // in place only row by row
+  if (S > 0 && ((q_out == q && !std::equal(p.qs, p.qs + 3, p.qos)) ||
+                (Hkv > 0 && k_out == k && !std::equal(p.ks, p.ks + 3, p.kos))))
+    return ATTN_ERR_INVALID_ARG;
   if (S == 0) return ATTN_OK;
   const int sms = sm_count();
   if (sms <= 0) return ATTN_ERR_CUDA;
@@ -181,6 +185,10 @@ int append_run(bool fp8, const void* q, const void* k, const void* v, void* q_ou
     const int bad = rope_check_strides(to[t], ext, 2);
     if (bad != ATTN_OK) return bad;
   }
+  // in place only when q is contiguous, as q_out is (strides of extents of one are 0)
+  if (total > 0 && q != nullptr && q_out == q &&
+      ((total > 1 && p.qs[0] != (long long)Hq * d) || (Hq > 1 && p.qs[1] != d)))
+    return ATTN_ERR_INVALID_ARG;
   if (total == 0) return ATTN_OK;
   const int sms = sm_count();
   if (sms <= 0) return ATTN_ERR_CUDA;

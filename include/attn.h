@@ -577,8 +577,9 @@ int attn_bwd_varlen(const void* q, const void* k, const void* v, const void* o, 
  *             themselves are contiguous; strides are multiples of 8 (16-byte
  *             pieces), not negative, and the outputs' rows may not overlap.
  *             Q and K may thus be views of a fused [B, S, heads, d] projection.
- *   q_out may be q with the same strides (in place), likewise k_out and k;
- *   any other overlap of an input with an output gives undefined values.
+ *   q_out may be q with the same strides (in place; with others the call is
+ *   refused), likewise k_out and k; any other overlap of an input with an
+ *   output gives undefined values.
  *   rotary_dim a multiple of 16 in [16, d]; d in {64, 128}; S >= 0; B * S <
  *   2^31; mscale finite.
  * Errors: INVALID_ARG, UNSUPPORTED (d, rotary_dim), ALIGNMENT, CUDA.
@@ -605,7 +606,7 @@ int attn_rope_bwd(const void* dq, const void* dk, void* dq_out, void* dk_out,
  *   k, v     [total, Hkv, d] bf16: the packed new tokens
  *   q        [total, Hq, d] bf16 or NULL (Hq = 0); q_out [total, Hq, d] bf16,
  *            contiguous, receives the rotated queries (may be q itself when q
- *            is contiguous)
+ *            is contiguous; refused otherwise)
  *   strides  HOST array of 6 element strides, (token, head) of q, k and v,
  *            multiples of 8 and not negative, or NULL when contiguous: the
  *            three may be views of one fused projection

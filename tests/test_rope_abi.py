@@ -67,6 +67,23 @@ def test_rope_validation(lib, fn, kw, status):
     assert _rope(lib, fn, **kw) == status
 
 
+@pytest.mark.parametrize("fn", ["attn_rope", "attn_rope_bwd"])
+@pytest.mark.parametrize("side", [0, 1])
+def test_rope_in_place_with_other_strides_is_refused(lib, fn, side):
+    """Q (or K) turned into its own memory in another order of heads and rows."""
+    S, d, H = 5, 128, (4, 2)[side]
+    s = _strides()
+    s[6 + 3 * side:9 + 3 * side] = [H * S * d, d, H * d]
+    kw = dict(q=FAKE, qo=FAKE, k=2 * FAKE, ko=3 * FAKE) if side == 0 else \
+        dict(q=FAKE, qo=3 * FAKE, k=2 * FAKE, ko=2 * FAKE)
+    assert _rope(lib, fn, strides=s, **kw) == B.ATTN_ERR_INVALID_ARG
+
+
+def test_append_in_place_of_strided_queries_is_refused(lib):
+    for s in ([1024, 128, 256, 128, 256, 128], [512, 256, 256, 128, 256, 128]):
+        assert _append(lib, q=FAKE, qo=FAKE, strides=s) == B.ATTN_ERR_INVALID_ARG
+
+
 def test_rope_of_no_rows_launches_nothing(lib):
     assert _rope(lib, S=0, q=None, k=None, qo=None, ko=None) == B.ATTN_OK
 
