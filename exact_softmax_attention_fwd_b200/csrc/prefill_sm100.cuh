@@ -553,7 +553,7 @@ __global__ void __launch_bounds__(384, 1)
     // the token-major tensor [num_pages * page_size, Hkv, d] (page p starts at
     // token p * page_size).  The barrier's byte count (valid pages, counted by
     // a ballot) is set by lane 0 before any copy is issued.
-    constexpr int kNoPage = INT_MIN;  // past the sequence's last page
+    constexpr int kNoPage = INT_MIN;  // past the sequence's last page, or not visible
     uint32_t kv = 0;                  // K/V tiles issued so far (ring position)
     bool ok = true;
     PrefillUnit u;
@@ -563,12 +563,21 @@ __global__ void __launch_bounds__(384, 1)
       const int n_lp = (u.klen + p.page_size - 1) / p.page_size;  // <= max_pages
       const int* tbl = p.block_table + (size_t)u.b * p.max_pages;
       const uint32_t row_off = (uint32_t)(lane * p.page_size * 128);
+      // With a window, pages that lie wholly between the first tokens and the
+      // lowest key of the unit's windows are no one's: they may have been given
+      // back, so that neither their table entries nor their rows are read.  The
+      // ring keeps earlier finite rows there, and the element masks hide them.
+      long long low_key = 0;
+      if (MASKS)
+        low_key = (long long)(u.row0[0] >> pack) + u.klen - (u.sq >> pack) - p.window + 1;
       for (int j = u.kv_first; j < u.kv_last; ++j, ++kv) {
         const int s = kv % C::STAGES;
         const uint32_t ph = (kv / C::STAGES) & 1u;
         const int tile = MASKS ? u.key_tile(j) : j;
         const int lp = tile * ppt + lane;
-        const int phys = (lane < ppt && lp < n_lp) ? __ldg(tbl + lp) : kNoPage;
+        const bool hidden = MASKS && (long long)(lp + 1) * p.page_size <= low_key &&
+                            (long long)lp * p.page_size >= p.sinks;
+        const int phys = (lane < ppt && lp < n_lp && !hidden) ? __ldg(tbl + lp) : kNoPage;
         const bool valid = phys >= 0 && phys < p.num_pages;
         if (phys != kNoPage && !valid) flag_device_error(kDevErrBadPage);  // skipped: its
         const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, valid)) *  // keys read

@@ -282,3 +282,47 @@ def test_other_stream_and_two_graphs():
     for out in outs:
         assert all(torch.equal(a, b) for a, b in zip(want, out))
     _ok()
+
+
+# new tokens and keys of two sequences, Hq, Hkv, d, page, window, first tokens: gaps of many tiles
+# and of less than one, the window's start and the first tokens' end inside a tile and a page,
+# one and several blocks of query rows, heads of a group in one tile (2, 4, 16) and not (1, 3)
+HIDDEN = [
+    ([10, 3], [1000, 700], 2, 1, 64, 16, 50, 4),
+    ([10, 3], [1000, 700], 4, 1, 128, 32, 50, 4),
+    ([10, 1], [1000, 700], 3, 1, 64, 64, 200, 0),
+    ([10, 40], [290, 300], 16, 1, 64, 16, 60, 4),      # the window starts in the tile after the first
+    ([5, 6], [120, 125], 1, 1, 128, 16, 20, 4),        # everything in one tile
+    ([5, 6], [120, 125], 4, 2, 128, 16, 20, 33),
+    ([300, 8], [900, 500], 2, 2, 128, 16, 100, 130),   # several blocks, two tiles of first tokens
+    ([300, 8], [900, 500], 8, 2, 64, 128, 100, 40),
+]
+
+
+@pytest.mark.parametrize("what", ["bad ids", "nan"])
+@pytest.mark.parametrize("case", HIDDEN, ids=str)
+def test_paged_pages_without_a_visible_key_are_not_read(case, what):
+    """Every page that lies wholly between the first tokens and the windows has an id outside the
+    pool, or holds NaN: the result keeps its bits, and nothing is flagged."""
+    new, total, Hq, Hkv, d, page, window, sinks = case
+    q, cu, c = W.paged_prefill_inputs(new, total, Hq, Hkv, d, page, 203)
+    args = _dev(q, c.k_cache, c.v_cache, c.block_table, cu, c.seq_lens)
+    scale = 1 / math.sqrt(d)
+    o, lse = attn_fwd_paged_window(*args, max(new), scale, window, sinks)
+    _ok()
+    check_rows(o, lse, S.paged_window(q, c.k_cache, c.v_cache, c.block_table, cu, c.seq_lens, scale,
+                                      window, sinks, bound=True), str(case))
+    kc, vc, table = c.k_cache.clone(), c.v_cache.clone(), c.block_table.clone()
+    n_hidden = 0
+    for b, (n, t) in enumerate(zip(new, total)):
+        for pg in range(-(-sinks // page), max(0, t - n - window + 1) // page):
+            n_hidden += 1
+            if what == "nan":
+                kc[int(table[b, pg])] = vc[int(table[b, pg])] = float("nan")
+            else:
+                table[b, pg] = c.num_pages + 7 if pg % 2 else -1
+    assert n_hidden > 0
+    o2, lse2 = attn_fwd_paged_window(*_dev(q, kc, vc, table, cu, c.seq_lens), max(new), scale,
+                                     window, sinks)
+    _ok()
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
