@@ -175,7 +175,8 @@ __global__ void __launch_bounds__(kWinWarps * 32, DecodeWinCfg<D, FP8>::CTAS4)
   }
   __syncwarp();
   w.begin(qraw, p.scale_log2);
-  float vmax = 1.f;  // E4M3: the unit of the accumulator (largest V scale met so far)
+  float vmax = FP8 ? 0.f : 1.f;  // E4M3: the unit of the accumulator (0: only zeros so far)
+  float vtop = 0.f;              // and the largest V scale met
   int it = 0;        // steps done: ring slot and phase
   bool ok = true;
   // 32 chunks at a time: each lane holds one chunk's page and scales
@@ -211,21 +212,27 @@ __global__ void __launch_bounds__(kWinWarps * 32, DecodeWinCfg<D, FP8>::CTAS4)
     int n_issued = 0;
     for (; n_issued < C::STAGES && n_issued < n_steps; ++n_issued) issue(n_issued);
     if (FP8) {
+      // The accumulator's unit is the round's own largest V scale, as the split
+      // kernel's is for its 512 tokens, so that the round's weights P * vs / unit
+      // keep their f16 precision whatever came before.  A round of zero scales keeps
+      // the unit, and none is below 2^-64 of the largest (the sums stay finite).
       float m = fabsf(my_vs);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      if (it == 0) {
-        if (m > 0.f) vmax = m;
-      } else if (m > vmax) {  // a larger unit from here on
-        const float r = vmax / m;
+      if (m > 0.f && m != vmax) {
+        vtop = fmaxf(vtop, m);
+        m = fmaxf(m, vtop * 0x1p-64f);
+        if (vmax > 0.f) {
+          const float r = vmax / m;
 #pragma unroll
-        for (int mc = 0; mc < D / 16; ++mc)
+          for (int mc = 0; mc < D / 16; ++mc)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) w.acc[mc][e] *= r;
+            for (int e = 0; e < 4; ++e) w.acc[mc][e] *= r;
+        }
         vmax = m;
       }
     }
-    const float my_rv = my_vs / vmax;
+    const float my_rv = FP8 && vmax > 0.f ? my_vs / vmax : 0.f;
     const float my_back = (FP8 && my_vs != 0.f) ? vmax / my_vs : 0.f;
     const float my_kq = my_ks * w.qscale;
     int i = 0;

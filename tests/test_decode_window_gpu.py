@@ -265,3 +265,28 @@ def test_refusals():
         attn_decode_paged_window(torch.zeros(2, 18, 64, dtype=torch.bfloat16, device=DEV), kc, vc,
                                  table, lens, 0.1, 4, 1)
     _ok()
+
+
+@pytest.mark.parametrize("small", [1e-5, 1e-6, 1e-8])
+@pytest.mark.parametrize("first", ["scale 0", "values 0"])
+def test_fp8_small_v_scales_behind_a_run_of_zeros(first, small):
+    """One sequence of 32 x 1536 tokens: 32 warps (8 CTAs of 4), each with three rounds of 512
+    tokens, the first of which adds nothing to the sums (V scales of 0, or of 1 over codes of 0, as a
+    page that was never quantised has them).  The scales of the others are small: their weights keep
+    their precision, as in the plain decode, which takes 512 tokens at a time."""
+    n, page = 32 * 1536, 64
+    c = _make([n], 4, 1, 64, page, 220, True)
+    c.v_scale.fill_(small)
+    for t in range(0, n, page):
+        if t % 1536 < 512:
+            pg = int(c.block_table[0, t // page])
+            c.v_scale[pg] = 0.0 if first == "scale 0" else 1.0
+            if first == "values 0":
+                c.v_cache[pg] = 0
+    ref = _ref(c, 0.125, 0, 0, True)
+    q, kc, vc, table, lens = (x.to(DEV) for x in (c.q, c.k_cache, c.v_cache, c.block_table, c.seq_lens))
+    plain = attn_decode_paged_fp8(q, kc, vc, c.k_scale.to(DEV), c.v_scale.to(DEV), table, lens, 0.125)
+    check_rows(*plain, ref, "plain decode")
+    o, lse = _call(c, 0.125, 0, 0, True)
+    _ok()
+    check_rows(o, lse, ref)
