@@ -309,3 +309,18 @@ def test_binding_refusals():
     with pytest.raises(AttnError):
         attn_append_paged(k, v, kc, vc, table, lens, cud, inv_freq=f[:4])   # 8 turned elements
     assert torch.equal(kc.cpu(), c.k_cache)
+
+
+def test_q_out_at_the_address_of_strided_queries_is_refused():
+    """q as a view of the fused projection, q_out contiguous from the same address: other rows
+    of q would be overwritten before they are read."""
+    Hq, Hkv, d, total = 4, 2, 64, [40, 9]
+    qkv, c, _ = _case([1, 1], total, Hq, Hkv, d, 16, 61, single=True)
+    x = qkv.to(DEV)
+    q, k, v = _split(x, Hq, Hkv)
+    q_out = x.view(-1)[:2 * Hq * d].view(2, Hq, d)
+    assert q_out.is_contiguous() and q_out.data_ptr() == q.data_ptr()
+    kc, vc = c.k_cache.to(DEV), c.v_cache.to(DEV)
+    with pytest.raises(ValueError, match="itself"):
+        attn_append_paged(k, v, kc, vc, c.block_table.to(DEV), c.seq_lens.to(DEV), q=q, q_out=q_out)
+    assert torch.equal(x.cpu(), qkv) and torch.equal(kc.cpu(), c.k_cache)

@@ -326,3 +326,21 @@ def test_paged_pages_without_a_visible_key_are_not_read(case, what):
                                      window, sinks)
     _ok()
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("d,window,sinks", [(128, 1024, 4), (64, 300, 200)])
+def test_long_rows_against_the_oracle(d, window, sinks):
+    """5000 rows: windows of several tiles, and first tokens whose gradients many query tiles
+    share out among units."""
+    q, k, v = W.prefill_inputs(1, 2, 1, 5000, 5000, d, 204)
+    do = W.grad_output(1, 2, 5000, d, 205)
+    scale = 1 / math.sqrt(d)
+    assert attn_bwd_window_sinks_workspace_size(1, 2, 1, 5000, 5000, d, window, sinks) > \
+        attn_bwd_window_sinks_workspace_size(1, 2, 1, 5000, 5000, d, window, 0)
+    qd, kd, vd, dod = _dev(q, k, v, do)
+    o, lse = attn_fwd_window_sinks(qd, kd, vd, scale, window, sinks)
+    got = attn_bwd_window_sinks(qd, kd, vd, o, lse, dod, scale, window, sinks)
+    _ok()
+    check_rows(o, lse, S.window_fwd(q, k, v, scale, window, sinks, bound=True))
+    for name, g, r in zip(("dq", "dk", "dv"), got, S.window_grads(q, k, v, do, scale, window, sinks)):
+        check_grad(g, r, what=name)
