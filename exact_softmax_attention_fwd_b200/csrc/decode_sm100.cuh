@@ -558,16 +558,18 @@ __global__ void __launch_bounds__(32, 8) attn_decode_split_tma_kernel(
   uint32_t qraw[D / 8];
   w.load_q(qraw, p.q, (size_t)b * p.Hq + hq0, p.group);
 
-  // this lane's chunk: its page (or -1 when the id is outside the pool, or
-  // past the split), which of its tokens count, and its scales
-  int my_page = -1;
+  // this lane's chunk: its first token in the pool (or -1 when the page's id is
+  // outside it, or past the split), which of its tokens count, and its scales.
+  // The place is worked out here, once: a remainder by the page size in every step
+  // cost one sequence of 8192 keys 3 us of 24 (E4M3 3.7 of 22).
+  int my_tok = -1;
   uint32_t my_vis = 0;
   float my_ks = 0.f, my_vs = 0.f;
   if (lane < n_chunks) {
     const int t = t_begin + 16 * lane;
     const int pg = p.block_table[(size_t)b * p.max_pages + t / p.page_size];
     if (pg >= 0 && pg < p.num_pages) {
-      my_page = pg;
+      my_tok = pg * p.page_size + t % p.page_size;
       my_vis = t_end - t >= 16 ? 0xFFFFu : (1u << (t_end - t)) - 1u;
       if (FP8) {
         my_ks = __ldg(f.k_scale + (size_t)pg * p.Hkv + kvh);
@@ -589,10 +591,7 @@ __global__ void __launch_bounds__(32, 8) attn_decode_split_tma_kernel(
   auto issue = [&](int i) {
     int tok[NH];
 #pragma unroll
-    for (int h = 0; h < NH; ++h) {
-      const int pg = __shfl_sync(0xffffffffu, my_page, NH * i + h);
-      tok[h] = pg < 0 ? -1 : pg * p.page_size + (t_begin + 16 * (NH * i + h)) % p.page_size;
-    }
+    for (int h = 0; h < NH; ++h) tok[h] = __shfl_sync(0xffffffffu, my_tok, NH * i + h);
     if (lane == 0) {
       const int slot = i % C::STAGES;
       decode_issue<D, FP8>(&tm_k, &tm_v, sbase + slot * C::STAGE, bars + 8u * slot, kvh, tok);

@@ -139,3 +139,14 @@ def test_fp8_scales_of_any_sign_and_zero():
     o, lse = _run(c2, scale)
     o_ref, lse_ref = _ref(c2, scale)
     check(o, o_ref, lse, lse_ref, what="fp8 scales of any sign")
+
+
+@pytest.mark.parametrize("page_size", [16, 48, 80, 112, 128, 240, 256])
+def test_pages_of_every_kind_of_size(page_size):
+    """Sizes that are no power of two or exceed a split's share of a page: chunks' places in the
+    pool and their scales, in every split."""
+    c = W.fp8_paged_inputs(torch.tensor([1, page_size - 1, page_size, page_size + 1, 1300]), 4, 2,
+                           128, page_size, seed=page_size, extra_pages=2)
+    o, lse = _run(c, 0.09)
+    o_ref, lse_ref = _ref(c, 0.09)
+    check(o, o_ref, lse, lse_ref, what=f"pages of {page_size}")

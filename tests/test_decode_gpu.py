@@ -164,3 +164,10 @@ def test_slots_past_the_length_never_reach_the_result():
     vc[unused[0]] = float("nan")
     o2, l2 = _run(W.PagedInputs(inp.q, kc, vc, inp.block_table, inp.seq_lens, 16), 0.088)
     assert torch.equal(o1, o2) and torch.equal(l1, l2)
+
+
+@pytest.mark.parametrize("page_size", [16, 48, 80, 112, 128, 240, 256])
+def test_pages_of_every_kind_of_size(page_size):
+    """Sizes that are no power of two or exceed a split's share of a page: chunks' places in the
+    pool, in every split."""
+    _case([1, page_size - 1, page_size, page_size + 1, 1300], 4, 2, 64, page_size, seed=page_size)
