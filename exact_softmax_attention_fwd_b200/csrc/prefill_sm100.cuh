@@ -886,48 +886,52 @@ __global__ void __launch_bounds__(384, 1)
       float l_run = 0.f;         // sum of P (f32)
       float lr_run = 0.f;        // sum of bf16(P)
 
-      for (int j = kb; j < ke; ++j) {
+      int j = kb;
+      if (MASKS && u.narrow && j < ke) {
+        if (!(ok = mbar_wait_warp(bar(C::B_SFULL + i), s_waits & 1u, abort_flag))) break;
+        ++s_waits;
+        tc_fence_after_sync();
+        // the first tokens' columns alone; nothing has been accumulated yet, so
+        // this sets the base and the sums
+        uint32_t x[32];
+        tmem_ld32_sync(t_s, x);
+        const uint32_t vis = low_bits(p.sinks);
+        float mx = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < kSinkCols; ++c) {
+          float v = __uint_as_float(x[c]);
+          if (!scale_pos) v *= p.scale_log2;
+          if (!(vis & (1u << c))) v = -INFINITY;
+          x[c] = __float_as_uint(v);
+          mx = fmaxf(mx, v);
+        }
+        m_run = mx * c2;
+        const float base = (m_run == -INFINITY) ? 0.f : m_run;
+        uint32_t pk[kSinkCols / 2];
+        float l0 = 0.f, l1 = 0.f, r0 = 0.f, r1 = 0.f;
+#pragma unroll
+        for (int c = 0; c < kSinkCols / 2; ++c) {
+          const float p0 = ex2(fmaf(__uint_as_float(x[2 * c]), c2, -base));
+          const float p1 = ex2(fmaf(__uint_as_float(x[2 * c + 1]), c2, -base));
+          pk[c] = pack_bf16x2(p0, p1);
+          l0 += p0;
+          l1 += p1;
+          add_bf16x2_halves(pk[c], r0, r1);
+        }
+        tmem_st16(t_s, pk);
+        l_run = l0 + l1;
+        lr_run = r0 + r1;
+        tmem_st_wait();
+        tc_fence_before_sync();
+        mbar_arrive(bar(C::B_PFULL + i));
+        ++j;
+      }
+      for (; j < ke; ++j) {
         if (MASKS && p.block_mask != nullptr && !prefill_block_on(p, u.b, hq_i, row0, kb, ke, j))
           continue;  // a block the mask switches off: no S, no P for it
         if (!(ok = mbar_wait_warp(bar(C::B_SFULL + i), s_waits & 1u, abort_flag))) break;
         ++s_waits;
         tc_fence_after_sync();
-        if (MASKS && u.narrow && j == kb) {
-          // the first tokens' columns alone; nothing has been accumulated yet, so
-          // this sets the base and the sums
-          uint32_t x[32];
-          tmem_ld32_sync(t_s, x);
-          const uint32_t vis = low_bits(p.sinks);
-          float mx = -INFINITY;
-#pragma unroll
-          for (int c = 0; c < kSinkCols; ++c) {
-            float v = __uint_as_float(x[c]);
-            if (!scale_pos) v *= p.scale_log2;
-            if (!(vis & (1u << c))) v = -INFINITY;
-            x[c] = __float_as_uint(v);
-            mx = fmaxf(mx, v);
-          }
-          m_run = mx * c2;
-          const float base = (m_run == -INFINITY) ? 0.f : m_run;
-          uint32_t pk[kSinkCols / 2];
-          float l0 = 0.f, l1 = 0.f, r0 = 0.f, r1 = 0.f;
-#pragma unroll
-          for (int c = 0; c < kSinkCols / 2; ++c) {
-            const float p0 = ex2(fmaf(__uint_as_float(x[2 * c]), c2, -base));
-            const float p1 = ex2(fmaf(__uint_as_float(x[2 * c + 1]), c2, -base));
-            pk[c] = pack_bf16x2(p0, p1);
-            l0 += p0;
-            l1 += p1;
-            add_bf16x2_halves(pk[c], r0, r1);
-          }
-          tmem_st16(t_s, pk);
-          l_run = l0 + l1;
-          lr_run = r0 + r1;
-          tmem_st_wait();
-          tc_fence_before_sync();
-          mbar_arrive(bar(C::B_PFULL + i));
-          continue;
-        }
         float s[128];
         {
           uint32_t u0[32], u1[32], u2[32], u3[32];
