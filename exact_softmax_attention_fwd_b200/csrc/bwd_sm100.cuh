@@ -1072,14 +1072,15 @@ __global__ void __launch_bounds__(384, 1)
       if (CAUSAL)
         kend = min(kend, max((long long)row + u.koff, MASKS ? (long long)p.prefix - 1 : -1LL) + 1);
       if (MASKS && p.window > 0) klo = max(0LL, (long long)row + u.koff - p.window + 1);
-      for (int n = 0; n < NI; ++n, ++it) {
-        if (MASKS && u.narrow && n == 0) {
-          // the first tokens' columns, which every row here sees: all in the first
-          // warpgroup's run; the second one only keeps step
-          const uint32_t vis = low_bits(p.sinks);
-          if (!(ok = mbar_wait_warp(bar(C::QB_SF + (it & 1)), (it >> 1) & 1u, abort_flag))) break;
+      int n = 0;
+      if (MASKS && u.narrow && NI > 0) {
+        // the first tokens' columns, which every row here sees: all in the first
+        // warpgroup's run; the second one only keeps step
+        const uint32_t vis = low_bits(p.sinks);
+        uint32_t x[32];
+        ok = mbar_wait_warp(bar(C::QB_SF + (it & 1)), (it >> 1) & 1u, abort_flag);
+        if (ok) {
           tc_fence_after_sync();
-          uint32_t x[32];
           if (wg == 0) {
             tmem_ld32_sync(tmem + lane_off + ((it & 1) ? C::Q_TM_S1 : C::Q_TM_S0), x);
 #pragma unroll
@@ -1088,7 +1089,9 @@ __global__ void __launch_bounds__(384, 1)
                          ? __float_as_uint(ex2(fmaf(__uint_as_float(x[c]), p.scale_log2, nl)))
                          : 0u;
           }
-          if (!(ok = mbar_wait_warp(bar(C::QB_DPF), it & 1u, abort_flag))) break;
+          ok = mbar_wait_warp(bar(C::QB_DPF), it & 1u, abort_flag);
+        }
+        if (ok) {
           tc_fence_after_sync();
           if (wg == 0) {
             uint32_t a[32], pk[16];
@@ -1104,8 +1107,11 @@ __global__ void __launch_bounds__(384, 1)
           }
           tc_fence_before_sync();
           mbar_arrive(bar(C::QB_DSF));
-          continue;
+          n = 1;
+          ++it;
         }
+      }
+      for (; ok && n < NI; ++n, ++it) {
         const int kt = key_tile(u, n);
         const long long t0 = (long long)kt * 128 + c0;  // this run's first key
         long long cm = kend - t0;  // visible iff cmin <= c < cmax
