@@ -952,7 +952,9 @@ def attn_append_paged(k, v, k_cache, v_cache, block_table, seq_lens, cu_seqlens=
     the paged cache [num_pages, page_size, Hkv, d], as the last ones of their sequences:
     seq_lens [B] counts them in, cu_seqlens [B+1] gives each sequence's tokens (None: one token
     per sequence).  K and, where given, q [total, Hq, d] are rotated on the way (inv_freq as
-    attn_rope; None: not at all).  Returns the rotated queries, contiguous, or None."""
+    attn_rope; None: not at all).  Returns the rotated queries, contiguous, or None; rows of
+    idle sequences (length 0) and of tokens behind the last sequence are not written, so that a
+    new result holds whatever its memory held there."""
     return _append("attn_append_paged", k, v, k_cache, v_cache, None, None, block_table, seq_lens,
                    cu_seqlens, q, inv_freq, positions, interleaved, mscale, q_out, stream)
 
@@ -1151,7 +1153,8 @@ def attn_decode_paged_window(q, k_cache, v_cache, block_table, seq_lens, scale: 
                              sinks: int = 0, out=None, lse=None, return_lse: bool = True,
                              stream=None):
     """Single-query attention over a paged cache with a sliding window (0: none) and the first
-    ``sinks`` tokens visible (layouts as attn_decode_paged; no workspace)."""
+    ``sinks`` tokens visible (layouts as attn_decode_paged; no workspace).  Where few sequences
+    see tens of thousands of keys each, attn_decode_paged is the faster call."""
     return _decode_window("attn_decode_paged_window", q, k_cache, v_cache, None, None, block_table,
                           seq_lens, scale, window, sinks, out, lse, return_lse, stream)
 

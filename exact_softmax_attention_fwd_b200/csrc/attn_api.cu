@@ -692,8 +692,9 @@ size_t bwd_workspace_bytes(int B, int Hq, int Sq) {
 // How the first tokens' far query tiles (those that see a key tile through its
 // first tokens alone) are dealt to units of the dK/dV kernel: chunks per key
 // tile, as long as an ordinary unit (the window's query tiles of the group),
-// but no more units than four for every SM (148 on a B200), which also bounds
-// the partial sums' memory.  0 chunks: no query tile is far, or one chunk would
+// but no more units than four for every SM (148 on a B200, counted here since the
+// workspace's size is asked for where no GPU need be), which also bounds the
+// partial sums' memory.  0 chunks: no query tile is far, or one chunk would
 // do, and the key tile's own unit walks them as well.
 struct BwdFar {
   int tiles, chunks, rows;

@@ -20,7 +20,11 @@
 // Measured (64 sequences, 32 query and 8 KV heads of 128, window 1024, 4 first
 // tokens): 48 us for 251 MB of visible bf16 keys and values, 5.2 TB/s, 0.80 of the
 // measured copy rate; one sequence 6.2 us, with a window of 128 4.8 us, about 2 us of
-// them the launch and the rest dependent loads (length, block table, rows).
+// them the launch and the rest dependent loads (length, block table, rows); over an
+// E4M3 cache the 64 sequences take 31 us (125 MB).  At most 8 CTAs share a (sequence,
+// KV head), so that few sequences with windows of tens of thousands of tokens leave
+// SMs idle, which the split kernel fills: 131072 keys, no window, one sequence of 8 KV
+// heads 173 us against its 103, of one KV head 177 against 34; 8192 keys 16 against 21.
 //
 // Chunks: the list of the first tokens' chunks, then the window's (a chunk that
 // both touch is listed once).  A 16-bit mask per chunk says which of its tokens

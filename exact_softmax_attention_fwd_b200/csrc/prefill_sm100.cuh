@@ -60,10 +60,12 @@
 //
 // With a sliding window a few first tokens may stay visible ("sinks"): a unit's
 // stream is then the tiles of those tokens followed by the window's, and with up
-// to 32 of them their tile is computed as 32 columns.  Measured on 2 x 32 heads x
-// 8192 rows, d = 128, window 1024: 324 us without, 340 us with 4 first tokens
-// (760 TFLOP/s over visible pairs, 0.46 of the measured 1648), against 2.4 us a
-// step of two tiles, the pace of the causal kernel, whose softmax bounds it.
+// to 32 of them their tile is computed as 32 columns, in front of the loop over the
+// others (a test in every step cost prefix masks at 32 x 8192 rows 540 us instead of
+// 529).  Measured on 2 x 32 heads x 8192 rows, d = 128, window 1024, at 1965 MHz:
+// 315 us without, 332 us with 4 first tokens (780 TFLOP/s over visible pairs, 0.47 of
+// the measured 1648).  A step of two tiles takes 2.4 us, the pace of the causal
+// kernel; the rest, about 4 us a unit, is its start and end and the narrow tile.
 //
 // Empty rows (no visible key) get O = 0 and LSE = -inf: the exponent base
 // falls back to 0 while the running max is -inf, so P = 2^-inf = 0 and l = 0.

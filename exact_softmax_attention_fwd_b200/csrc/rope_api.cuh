@@ -13,7 +13,7 @@ namespace {
 // long runs of heads are cheapest when there are tokens enough), and one head
 // when there are few tokens.  Measured: the rotation of 8192 tokens x 40 heads
 // takes 29.4 us with 8 blocks an SM, 30.5 with 16, 31.0 with 32; the append of
-// 8300 tokens x 48 heads, whose blocks begin with a chain of look-ups, 48.8,
+// 10341 tokens x 48 heads, whose blocks begin with a chain of look-ups, 48.8,
 // 48.6 and 47.6, and 46.9 us with 24.
 constexpr int kRopeBlocks = 8, kAppendBlocks = 24;
 

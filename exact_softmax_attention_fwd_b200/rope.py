@@ -14,7 +14,9 @@ base frequencies f_i = base^(-i/n):
                 r_i = original_length f_i / 2 pi: pairs with r_i >= fast_turns
                 keep f_i, pairs with r_i <= slow_turns get f_i / factor, and the
                 share of f_i falls linearly in r_i between the two; ``mscale``
-                is 0.1 ln(factor) + 1
+                is 0.1 ln(factor) + 1.  Models trained with a ramp over the
+                pair's index i instead (between bounds rounded to whole pairs)
+                have other frequencies: pass their own table
 """
 from __future__ import annotations
 

@@ -626,7 +626,8 @@ int attn_rope_bwd(const void* dq, const void* dk, void* dq_out, void* dk_out,
  *            nothing turns (mscale is not applied either)
  *   page_size a positive multiple of 16 (<= 256); d in {64, 128}.
  *   Two tokens with the same place (a page listed twice) are written in no
- *   fixed order.  Tokens behind the last sequence are left alone, as are
+ *   fixed order; any other overlap of an input with an output gives undefined
+ *   values.  Tokens behind the last sequence are left alone, as are
  *   their q_out rows, and every other slot of the cache.
  * Device-side faults: a page id outside [0, num_pages) is skipped (its keys
  * and values are not written) and flags ATTN_DEVERR_BAD_PAGE; a sequence whose
@@ -739,7 +740,8 @@ int attn_bwd_window_sinks(const void* q, const void* k, const void* v, const voi
  * visible may hold anything.
  *   seq_lens 0 is allowed (O = 0, LSE = -inf).  No workspace: one kernel, a
  *   cluster of 1 to 8 CTAs per (sequence, KV head), which merges its warps'
- *   parts in shared memory in a fixed order.
+ *   parts in shared memory in a fixed order.  Where few sequences see tens of
+ *   thousands of keys each, attn_decode_paged fills the GPU better.
  *   page_size a positive multiple of 16 (<= 256); d in {64, 128};
  *   Hq / Hkv <= 8; B * Hkv <= 2^27.
  * Other arguments, layouts, device-side checks and errors as
