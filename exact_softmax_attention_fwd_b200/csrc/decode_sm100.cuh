@@ -36,8 +36,11 @@
 // P before P is rounded to f16 (vmax = the largest V scale magnitude of the
 // split's pages), and the accumulator, in units of vmax, is multiplied by vmax
 // once at the end.  The normaliser sums the weights as applied to the
-// dequantised V, f16(P') * vmax / vs per token (f16(P) on a page whose scale
-// is zero).
+// dequantised V, f16(P') * vmax / vs per token.  A page whose scale is below a
+// 16th of vmax (a zero one too) keeps f16(P) as its weights, since P * vs / vmax
+// would leave f16's normal range (at 2^-20 weights are off by percents, at 2^-25
+// they vanish, from the normaliser as well), and the accumulator is taken over
+// to that page's unit and back around its products.
 //
 // Rescaling is lazy, as in the prefill kernel: the exponent base of a head
 // row moves only when the row max exceeds it by more than 8 (log2 units), so
@@ -228,6 +231,18 @@ __device__ __forceinline__ void ldsm_m16n16_trans_b8(uint32_t (&r)[2], uint32_t 
                : "r"(addr));
 }
 
+// E4M3 caches: the factor vs / vmax of a chunk enters its weights, before they are
+// rounded to f16, where it is a 16th or more in magnitude (so P down to 2^-10 stays
+// among f16's normal numbers, and none above 2^-21 vanishes), and its products below
+// that.  Products below 2^-64 of the unit are left out, as a zero scale's are (the
+// sum, of up to 2^30 products of 2^17, stays finite in the chunk's unit).
+constexpr float kDecodeFold = 0.0625f, kDecodeNone = 0x1p-64f;
+
+// That factor (vmax = 0: nothing but zeros so far), and 1 for a chunk that is not read.
+__device__ __forceinline__ float decode_v_rel(bool read, float vs, float vmax) {
+  return !read ? 1.f : vmax > 0.f ? vs / vmax : 0.f;
+}
+
 // The state of one warp that attends the query heads of one KV head, 16 tokens
 // (a chunk) at a time: the MMA operand q, the online softmax of head row g, and
 // the accumulator O^T.  Used by the split kernel below and by the windowed
@@ -306,12 +321,13 @@ struct DecodeWarp {
 
   // One step: NH chunks whose K and V rows lie in the ring slot at `st`.
   // vis[h]: bit i is set iff token i of chunk h counts (others may hold
-  // anything).  E4M3 caches: kqc, rvc, backc as described at the split kernel.
-  // `read_done` runs as soon as the warp has read the slot.
+  // anything).  E4M3 caches: kqc as described at the split kernel; rel[h]: chunk h's
+  // V scale over the accumulator's unit (decode_v_rel).  `read_done` runs as soon as
+  // the warp has read the slot.
   template <typename ReadDone>
   __device__ __forceinline__ void step(uint32_t st, float scale_log2, const uint32_t (&vis)[NH],
-                                       const float (&kqc)[NH], const float (&rvc)[NH],
-                                       const float (&backc)[NH], ReadDone read_done) {
+                                       const float (&kqc)[NH], const float (&rel)[NH],
+                                       ReadDone read_done) {
     // ---- S = q K^T (16 padded head rows x 16 tokens per chunk); two
     // independent accumulation chains (even and odd d-chunks), summed
     float s4[NH][4];
@@ -383,10 +399,12 @@ struct DecodeWarp {
     }
     const float base = (m_run == -INFINITY) ? 0.f : m_run;
     // P^T rows (tokens) 2tq, 2tq+1 and 2tq+8, 2tq+9 of each chunk, column g
-    // (head): bf16 for a bf16 cache; for an E4M3 cache f16 of P * vs / vmax
-    // (<= 2^8), and the weights on the dequantised V are f16(P') * vmax / vs
+    // (head): bf16 for a bf16 cache; for an E4M3 cache f16 of P' = P * vs / vmax
+    // (<= 2^8), whose weights on the dequantised V are f16(P') * vmax / vs, or of P
+    // where that factor is below a 16th
     uint32_t pb[NH][2];
     float rs = 0.f, rr = 0.f;
+    bool apart = false;
 #pragma unroll
     for (int h = 0; h < NH; ++h) {
       float pr[4];
@@ -398,18 +416,15 @@ struct DecodeWarp {
         pb[h][1] = pack_bf16x2(pr[2], pr[3]);
         rr += sum_f32x2(add_f32x2(bf16x2_to_f32x2(pb[h][0]), bf16x2_to_f32x2(pb[h][1])));
       } else {
-        const float rv = rvc[h];  // |rv| <= 1, the sign of the scale
+        const float v = rel[h];
+        const bool folds = fabsf(v) >= kDecodeFold;
+        apart = apart || !folds;
+        const float rv = folds ? v : 1.f;
         pb[h][0] = pack_f16x2(pr[0] * rv, pr[1] * rv);
         pb[h][1] = pack_f16x2(pr[2] * rv, pr[3] * rv);
-        if (backc[h] != 0.f) {
-          rr += ((f16_to_f32(pb[h][0]) + f16_to_f32(pb[h][0] >> 16)) +
-                 (f16_to_f32(pb[h][1]) + f16_to_f32(pb[h][1] >> 16))) * backc[h];
-        } else {
-          // a zero scale: the page's values add nothing, but its weights still
-          // count in the normaliser (as f16, the rounding of the other pages)
-          const uint32_t w0 = pack_f16x2(pr[0], pr[1]), w1 = pack_f16x2(pr[2], pr[3]);
-          rr += (f16_to_f32(w0) + f16_to_f32(w0 >> 16)) + (f16_to_f32(w1) + f16_to_f32(w1 >> 16));
-        }
+        rr += ((f16_to_f32(pb[h][0]) + f16_to_f32(pb[h][0] >> 16)) +
+               (f16_to_f32(pb[h][1]) + f16_to_f32(pb[h][1] >> 16))) *
+              __fdividef(1.f, rv);  // to 2^-22, far below the weights' 2^-11
       }
     }
     l_run = l_run * alpha + rs;
@@ -479,21 +494,40 @@ struct DecodeWarp {
         acc[mc][3] *= a_h1;
       }
     }
-#pragma unroll
-    for (int mc = 0; mc < D / 16; ++mc) {
+    auto product = [&](int h, int mc) {
+      if constexpr (!FP8) {
+        mma_m16n8k16_bf16(acc[mc], vw[h][mc][0], vw[h][mc][1], vw[h][mc][2], vw[h][mc][3], pb[h][0],
+                          pb[h][1]);
+      } else {
+        uint32_t a0, a1, a2, a3;
+        e4m3x4_to_f16x2x2(vw[h][mc][0], a0, a2);
+        e4m3x4_to_f16x2x2(vw[h][mc][1], a1, a3);
+        mma_m16n8k16_f16(acc[mc], a0, a1, a2, a3, pb[h][0], pb[h][1]);
+      }
+    };
+    if (FP8 && apart) {
+      // some chunk's weights are P: the sum is taken over to its unit and back
 #pragma unroll
       for (int h = 0; h < NH; ++h) {
-        if constexpr (!FP8) {
-          mma_m16n8k16_bf16(acc[mc], vw[h][mc][0], vw[h][mc][1], vw[h][mc][2], vw[h][mc][3],
-                            pb[h][0], pb[h][1]);
-        } else {
-          uint32_t a0, a1, a2, a3;
-          e4m3x4_to_f16x2x2(vw[h][mc][0], a0, a2);
-          e4m3x4_to_f16x2x2(vw[h][mc][1], a1, a3);
-          mma_m16n8k16_f16(acc[mc], a0, a1, a2, a3, pb[h][0], pb[h][1]);
+        const float v = rel[h];
+        const bool folds = fabsf(v) >= kDecodeFold;
+        if (fabsf(v) < kDecodeNone) continue;
+        const float to = folds ? 1.f : 1.f / v, back = folds ? 1.f : v;
+#pragma unroll
+        for (int mc = 0; mc < D / 16; ++mc) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[mc][e] *= to;
+          product(h, mc);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[mc][e] *= back;
         }
       }
+      return;
     }
+#pragma unroll
+    for (int mc = 0; mc < D / 16; ++mc)
+#pragma unroll
+      for (int h = 0; h < NH; ++h) product(h, mc);
   }
 
   // The row sums were kept per lane: every lane of a head row shares its base.
@@ -606,12 +640,7 @@ __global__ void __launch_bounds__(32, 8) attn_decode_split_tma_kernel(
     for (int o = 16; o > 0; o >>= 1) vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, o));
     if (!(vmax > 0.f)) vmax = 1.f;
   }
-  const float inv_vmax = FP8 ? 1.f / vmax : 1.f;
-  // E4M3: this lane's chunk's factor on P (|.| <= 1) and the factor that takes
-  // the applied weights back to weights on the dequantised V (0 marks a zero
-  // scale, whose weights count as f16(P))
-  const float my_rv = my_vs * inv_vmax;
-  const float my_back = (FP8 && my_vs != 0.f) ? vmax / my_vs : 0.f;
+  const float my_rel = decode_v_rel(my_tok >= 0, my_vs, vmax);
 
   w.begin(qraw, p.scale_log2);
   const float my_kq = my_ks * w.qscale;  // E4M3: K scale times the power of two on q
@@ -621,18 +650,17 @@ __global__ void __launch_bounds__(32, 8) attn_decode_split_tma_kernel(
   for (; i < n_steps; ++i) {
     const int slot = i % C::STAGES;
     uint32_t vis[NH];
-    float kqc[NH], rvc[NH], backc[NH];
+    float kqc[NH], rel[NH];
 #pragma unroll
     for (int h = 0; h < NH; ++h) {
       const int c = NH * i + h;
       vis[h] = __shfl_sync(0xffffffffu, my_vis, c);
       kqc[h] = FP8 ? __shfl_sync(0xffffffffu, my_kq, c) : 1.f;
-      rvc[h] = FP8 ? __shfl_sync(0xffffffffu, my_rv, c) : 1.f;
-      backc[h] = FP8 ? __shfl_sync(0xffffffffu, my_back, c) : 1.f;
+      rel[h] = FP8 ? __shfl_sync(0xffffffffu, my_rel, c) : 1.f;
     }
     const bool landed = mbar_wait(bars + 8u * slot, (uint32_t)(i / C::STAGES) & 1u, nullptr);
     if (!__all_sync(0xffffffffu, landed)) break;  // timed out: flagged, wind down
-    w.step(sbase + slot * C::STAGE, p.scale_log2, vis, kqc, rvc, backc, [&] {
+    w.step(sbase + slot * C::STAGE, p.scale_log2, vis, kqc, rel, [&] {
       if (n_issued < n_steps) issue(n_issued++);  // refill the slot with step i + C::STAGES
     });
   }

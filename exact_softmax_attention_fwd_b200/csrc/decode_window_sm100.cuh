@@ -236,22 +236,20 @@ __global__ void __launch_bounds__(kWinWarps * 32, DecodeWinCfg<D, FP8>::CTAS4)
         vmax = m;
       }
     }
-    const float my_rv = FP8 && vmax > 0.f ? my_vs / vmax : 0.f;
-    const float my_back = (FP8 && my_vs != 0.f) ? vmax / my_vs : 0.f;
+    const float my_rel = decode_v_rel(my_tok >= 0, my_vs, vmax);
     const float my_kq = my_ks * w.qscale;
     int i = 0;
 #pragma unroll 1
     for (; i < n_steps; ++i) {
       const int slot = (it + i) % C::STAGES;
       uint32_t vis[NH];
-      float kqc[NH], rvc[NH], backc[NH];
+      float kqc[NH], rel[NH];
 #pragma unroll
       for (int h = 0; h < NH; ++h) {
         const int c = NH * i + h;
         vis[h] = __shfl_sync(0xffffffffu, my_vis, c);
         kqc[h] = FP8 ? __shfl_sync(0xffffffffu, my_kq, c) : 1.f;
-        rvc[h] = FP8 ? __shfl_sync(0xffffffffu, my_rv, c) : 1.f;
-        backc[h] = FP8 ? __shfl_sync(0xffffffffu, my_back, c) : 1.f;
+        rel[h] = FP8 ? __shfl_sync(0xffffffffu, my_rel, c) : 1.f;
       }
       const bool landed =
           mbar_wait(bars + 8u * slot, (uint32_t)((it + i) / C::STAGES) & 1u, nullptr);
@@ -259,7 +257,7 @@ __global__ void __launch_bounds__(kWinWarps * 32, DecodeWinCfg<D, FP8>::CTAS4)
         ok = false;
         break;
       }
-      w.step(ring + slot * C::STAGE, p.scale_log2, vis, kqc, rvc, backc, [&] {
+      w.step(ring + slot * C::STAGE, p.scale_log2, vis, kqc, rel, [&] {
         if (n_issued < n_steps) issue(n_issued++);
       });
     }

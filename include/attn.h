@@ -424,9 +424,11 @@ int attn_decode_paged_noalloc(const void* q, const void* k_cache, const void* v_
  *   The attention computed is attn_decode_paged's over those dequantised
  *   values.  The kernel widens the codes exactly to f16 for two f16 MMAs:
  *   q K^T with q multiplied by a power of two into f16's range (exact for bf16
- *   q down to f16's subnormals), and P V with P rounded to f16; the K scale
- *   (and that power of two) multiply the fp32 scores, the V scale each page's
- *   fp32 partial output.
+ *   q down to f16's subnormals), and P V with P rounded to f16 (times the
+ *   page's V scale over the largest one of its 512 tokens where that is a 16th
+ *   or more, so that weights below 2^-21 of a row's largest may vanish); the K
+ *   scale (and that power of two) multiply the fp32 scores, a smaller V scale its
+ *   page's fp32 products (one below 2^-64 of that largest one counts as 0).
  * Other arguments, workspace (attn_decode_workspace_size), device-side
  * checks and errors as attn_decode_paged; INVALID_ARG also for a NULL scale
  * array, ALIGNMENT when a scale array is not 4-byte aligned (the caches need

@@ -150,3 +150,47 @@ def test_pages_of_every_kind_of_size(page_size):
     o, lse = _run(c, 0.09)
     o_ref, lse_ref = _ref(c, 0.09)
     check(o, o_ref, lse, lse_ref, what=f"pages of {page_size}")
+
+
+@pytest.mark.parametrize("spread", [16, 1e3, 1e6, 1e11])
+@pytest.mark.parametrize("d", [64, 128])
+def test_fp8_v_scales_far_apart_within_a_split(d, spread):
+    """V scales of pages next to one another that differ by up to `spread`, zeros and both signs
+    among them: every row within the bound of weights rounded to 8 bits, tokens of small scales
+    keeping their weight in the normaliser."""
+    from oracle.kv_fp8 import dequantize
+    from oracle.serving import paged_window
+    from window_parity import check_rows
+    c = W.fp8_paged_inputs(torch.tensor([1300, 97, 530, 16], dtype=torch.int32), 8, 2, d, 16, seed=45)
+    g = torch.Generator().manual_seed(46)
+    f = torch.tensor([0.0, 1.0, -1.0, 1 / spread, -1 / spread, spread ** -0.5])
+    c.v_scale.mul_(f[torch.randint(0, len(f), c.v_scale.shape, generator=g)])
+    o, lse = _run(c, 1 / math.sqrt(d))
+    kc, vc = dequantize(c.k_cache, c.k_scale), dequantize(c.v_cache, c.v_scale)
+    check_rows(o, lse, paged_window(c.q, kc, vc, c.block_table, None, c.seq_lens, 1 / math.sqrt(d),
+                                    0, 0, bound=True), f"spread {spread}")
+    # one page far above the others, met by almost no weight: the others keep theirs
+    c = W.fp8_paged_inputs(torch.tensor([500], dtype=torch.int32), 4, 1, d, 16, seed=47)
+    c.q.fill_(1.0)
+    c.k_scale.fill_(0.0)
+    page = int(c.block_table[0, 7])
+    c.k_scale[page] = 0.01
+    c.k_cache[page] = 0xC0                       # -2: every score -0.02 d scale
+    c.v_scale.fill_(1 / spread)
+    c.v_scale[page] = 1.0
+    scale = 20.0 / (0.02 * d)                    # 20 below the other scores
+    o, lse = _run(c, scale)
+    kc, vc = dequantize(c.k_cache, c.k_scale), dequantize(c.v_cache, c.v_scale)
+    ref = paged_window(c.q, kc, vc, c.block_table, None, c.seq_lens, scale, 0, 0, bound=True)
+    if spread < 1e10:
+        check_rows(o, lse, ref, f"one page, spread {spread}")
+    # At 1e11 that page, of weights e^-20 = 2^-29 of the others', makes up most of the row.  A
+    # weight is f16 of P vs / vmax with |vs / vmax| >= 2^-4, or of P: off by up to 2^-25 (half of
+    # f16's smallest step) / 2^-4 = 2^-21 of the largest P, which is at least 1, beside the
+    # bound's share of its value.  The largest normalised weight is below 1 / 484, so an element
+    # is off by up to 2^-21 / 484 * sum_j (|v_j| + |o|) more (the second part: the normaliser).
+    ro, rl, tol = ref
+    seen = vc[c.block_table[0, :32].numpy()].reshape(-1, d)[:500]
+    floor = 2.0 ** -21 / 484 * (np.abs(seen).sum(0) + 500 * np.abs(ro))
+    assert (np.abs(o.double().numpy() - ro) <= tol + floor).all()
+    assert np.abs(lse.double().numpy() - rl).max() <= 1e-3

@@ -290,3 +290,17 @@ def test_fp8_small_v_scales_behind_a_run_of_zeros(first, small):
     o, lse = _call(c, 0.125, 0, 0, True)
     _ok()
     check_rows(o, lse, ref)
+
+
+@pytest.mark.parametrize("spread", [16, 1e3, 1e6, 1e11])
+@pytest.mark.parametrize("lens,window", [([3000, 40], 0), ([900] * 40, 700)])
+def test_fp8_v_scales_far_apart_within_a_warps_run(lens, window, spread):
+    """V scales of pages next to one another that differ by up to `spread`, zeros and both signs
+    among them: as the plain decode."""
+    c = _make(lens, 4, 2, 128, 16, 221, True)
+    g = torch.Generator().manual_seed(222)
+    f = torch.tensor([0.0, 1.0, -1.0, 1 / spread, -1 / spread, spread ** -0.5])
+    c.v_scale.mul_(f[torch.randint(0, len(f), c.v_scale.shape, generator=g)])
+    o, lse = _call(c, 0.088, window, 4, True)
+    _ok()
+    check_rows(o, lse, _ref(c, 0.088, window, 4, True), f"spread {spread}")
