@@ -140,7 +140,9 @@ int attn_fwd_host(const void* q, const void* k, const void* v, void* o, float* l
  *   o [B, Hq, Sq, d] bf16 and lse [B, Hq, Sq] fp32 (nullable) are written as
  *   by attn_fwd_masked; causal, scale, k_lens likewise.
  *   d must be 128.  S = Q K^T runs on E4M3 tensor-core MMAs (the two block
- *   scales enter the fp32 scores); P V runs in bf16 on V widened exactly.
+ *   scales enter the fp32 scores); P V runs in f16 on V widened exactly, P times
+ *   the V block's scale over the largest one among the query tile's keys: values of
+ *   blocks whose scale is below 2^-14 of that lose bits (not their weight).
  * Errors: as attn_fwd_masked, plus INVALID_ARG for a NULL scale array,
  * UNSUPPORTED for d != 128, ALIGNMENT for scales not 4-byte aligned.
  */
